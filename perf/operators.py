@@ -263,7 +263,7 @@ def _own(s):
     if s["form"] == "up":
         x = tdt.moe_gather_mx4(s["x"], s["k"], s["inv"], s["C"])
     else:
-        x = tdt.moe_quantize_mx4(s["x"])
+        x = tdt.moe_quantize_mx4(s["x"], num_rows=s["n_pad"])
     w = tdt.Mx4Tensor(s["qw"].view(El * N, K // 2), s["sw"])
     return tdt.moe_grouped_gemm_mx4(x, w, s["counts"], s["offsets"], out=s["y"], swiglu=s["form"] == "up")
 
