@@ -8,8 +8,11 @@
  *   moe_gather         activation permute-gather into the expert-grouped layout
  *   moe_combine        top-k weighted combine back to token order
  * Between moe_gather and moe_combine the caller runs its expert MLPs on the
- * expert-grouped rows; they are not part of this library.  Under expert
+ * expert-grouped rows: its own, or in microscaled 4-bit floating point
+ * moe_gather_mx4 (or moe_quantize_mx4) and moe_grouped_gemm_mx4.  Under expert
  * parallelism, moe_reduce_partials sums the ranks' partial combines.
+ * For training, the gradients of the combine, the gather and the gating are
+ * moe_combine_backward, moe_gather_backward and moe_topk_softmax_backward.
  *
  * Sources (web pages, by title and section):
  *   "project_6/upstream_ref -- Upstream Reference: Deep-Spark xllm + vllm":
@@ -94,6 +97,8 @@ typedef enum { MOE_DTYPE_F32 = 0, MOE_DTYPE_BF16 = 1 } moe_dtype_t;
                                    (the sigmoid variant of the gating); the selection is the same */
 #define MOE_DISPATCH_GIVEN_IDS 8u /* moe_route_dispatch: topk_ids is an input (routes chosen by the
                                      caller); no gating, logits and topk_weights are not accessed */
+
+#define MOE_MX4_SWIGLU 32u /* moe_grouped_gemm_mx4: out = silu(first half of the features) * second half */
 
 /* Human-readable name of a status code (static string, never NULL). */
 MOE_API const char* moe_status_string(moe_status_t status);
@@ -315,6 +320,105 @@ MOE_API moe_status_t moe_route_dispatch(const void* logits, moe_dtype_t dtype, c
  */
 MOE_API moe_status_t moe_reduce_partials(const void* const* partials, int32_t n_partials, int64_t rows, int32_t H,
                                          void* out, void* stream);
+
+/*
+ * moe_combine_backward -- gradient of moe_combine: with r = inv_perm[t*k+j] >= 0 and grad_out = dL/d out,
+ *   grad_expert_out[r,h]    = bf16_rne(topk_weights[t,j] * grad_out[t,h])
+ *   grad_topk_weights[t,j]  = sum_h grad_out[t,h] * expert_out[r,h], summed in fp32; 0 for a remote slot.
+ *   grad_out [T, H] bf16; expert_out, grad_expert_out [capacity, H] bf16; topk_weights, grad_topk_weights [T, k] fp32.
+ *   grad_expert_out or grad_topk_weights may be NULL (not wanted); without grad_topk_weights expert_out is not read
+ *   and may be NULL.  grad_expert_out may be expert_out itself (each element is read before it is written); no other
+ *   overlap is allowed.
+ *   flags: MOE_GATHER_ZERO_PAD writes +0 into every pad row of grad_expert_out below N_pad (needs sorted_token_ids and
+ *   num_tokens_post_pad, which may otherwise be NULL), so that products over the padded blocks add nothing.  Without
+ *   it pad rows, and always the rows from N_pad on, are left as they were.
+ *   inv_perm's rows must be distinct (as moe_align_permute makes them).
+ *   Deterministic.  device_status: as for moe_gather.
+ *   Errors: INVALID_ARG (sizes, null or misaligned pointers, H % 8 != 0, both outputs NULL), UNSUPPORTED (k > 32).
+ */
+MOE_API moe_status_t moe_combine_backward(const void* grad_out, const void* expert_out, const float* topk_weights,
+                                          const int32_t* inv_perm, const int32_t* sorted_token_ids,
+                                          const int32_t* num_tokens_post_pad, int64_t T, int32_t k, int32_t H,
+                                          int64_t capacity, uint32_t flags, void* grad_expert_out,
+                                          float* grad_topk_weights, int32_t* device_status, void* stream);
+
+/*
+ * moe_gather_backward -- gradient of moe_gather: grad_hidden[t,h] = bf16_rne(sum over the local slots j of
+ *   grad_permuted[inv_perm[t*k+j], h]), summed in fp32 in slot order from +0; +0 for a token with no local slot.
+ *   grad_permuted [capacity, H] bf16 (pad rows are not read); grad_hidden [T, H] bf16.
+ *   Errors and device_status: as for moe_combine.
+ */
+MOE_API moe_status_t moe_gather_backward(const void* grad_permuted, const int32_t* inv_perm, int64_t T, int32_t k,
+                                         int32_t H, int64_t capacity, void* grad_hidden, int32_t* device_status,
+                                         void* stream);
+
+/*
+ * moe_topk_softmax_backward -- gradient of moe_topk_softmax's weights with respect to the logits; the selection is
+ * a constant.  With g_j = grad_topk_weights[t,j], w_j = topk_weights[t,j], i_j = topk_ids[t,j] and G = sum_j g_j w_j:
+ *   softmax                       grad_logits[t,e]   = p_e (g_e - G), p = softmax(logits[t]), g_e = 0 if not selected
+ *   softmax, MOE_RENORMALIZE      grad_logits[t,i_j] = w_j (g_j - G), 0 elsewhere; logits is not read and may be NULL
+ *   MOE_SCORING_SIGMOID           grad_logits[t,i_j] = w_j (1 - s_j) g_j, 0 elsewhere, s_j the logistic of the logit
+ *   both flags                    grad_logits[t,i_j] = w_j (1 - s_j) (g_j - G), 0 elsewhere
+ *                                 (0 everywhere if every s_j underflowed to 0: the weights are then the constant 1/k)
+ *   dtype: of logits and grad_logits [T, E]; topk_weights and topk_ids as moe_topk_softmax returned them with the same
+ *   flags.  Computed in fp32, one rounding to dtype.  The gradients of an expert named twice in a row add up.  An id
+ *   outside [0, E) is left out and MOE_ERR_BAD_EXPERT_ID recorded in device_status (a device int32 or NULL).
+ *   grad_logits may be logits itself.  Errors: as for moe_topk_softmax.
+ */
+MOE_API moe_status_t moe_topk_softmax_backward(const float* grad_topk_weights, const void* logits,
+                                               moe_dtype_t dtype, const float* topk_weights,
+                                               const int32_t* topk_ids, int64_t T, int32_t E, int32_t k,
+                                               uint32_t flags, void* grad_logits, int32_t* device_status,
+                                               void* stream);
+
+/*
+ * Microscaled 4-bit floating point (MXFP4 of the OCP Microscaling Formats specification v1.0).  32 consecutive
+ * elements of a row share a scale 2^s, the byte s + 127 (255: NaN); an element is a 4-bit E2M1 code, one of
+ * 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives, times 2^s.  A matrix [rows, K], K % 32 == 0, is
+ *   codes   [rows, K/2] bytes, element 2i in the low half of byte i and element 2i+1 in the high half;
+ *   scales  [ceil(K/128), rows, 4] bytes: scales[c, r, i] is the scale of row r's block 4c + i (127 past K).
+ * Both 16-byte aligned.
+ *
+ * moe_quantize_mx4: x [rows, K] bf16 -> codes, scales.  s = clamp(floor(log2(max |x| of the block)) - 2, -127, 127);
+ *   each x 2^-s to the nearest value, ties to the even code, saturating at 6.  A block that holds an infinity or a
+ *   NaN reads back as 32 NaN; a block of zeros has scale byte 0.  num_rows: a device int32, or NULL for all: rows
+ *   from *num_rows on are neither read nor written (num_tokens_post_pad where x holds expert-grouped rows).
+ * moe_dequantize_mx4: codes, scales -> out [rows, K] bf16: each value rounded once (exact for every scale byte that
+ *   moe_quantize_mx4 writes).
+ * moe_gather_mx4: moe_gather and moe_quantize_mx4 in one: row inv_perm[s] of codes [capacity, H/2] and
+ *   scales [ceil(H/128), capacity, 4] becomes the quantised hidden row s / k, for every local slot s.  A token's row
+ *   is read and quantised once, not at all without a local slot.  Other rows are left as they were.
+ * Errors: INVALID_ARG (sizes, K or H % 32 != 0 or beyond 2^20, 2^31 rows, null or misaligned pointers), UNSUPPORTED
+ *   (k > 32, more than 2^33 / 256 pieces of rows).  device_status: as for moe_gather.
+ */
+MOE_API moe_status_t moe_quantize_mx4(const void* x, int64_t rows, int32_t K, const int32_t* num_rows, void* codes,
+                                      void* scales, void* stream);
+MOE_API moe_status_t moe_dequantize_mx4(const void* codes, const void* scales, int64_t rows, int32_t K, void* out,
+                                        void* stream);
+MOE_API moe_status_t moe_gather_mx4(const void* hidden, int64_t T, int32_t H, int32_t k, const int32_t* inv_perm,
+                                    int64_t capacity, void* codes, void* scales, int32_t* device_status,
+                                    void* stream);
+
+/*
+ * moe_grouped_gemm_mx4 -- the experts' matrix product on expert-grouped rows ("gemm1" and "gemm2" of the FusedMoE
+ * pipeline, with the "act" between them fused on request; "Upstream Reference", "File Index"):
+ *   out[r,n] = bf16_rne(sum_k x[r,k] * w[e,n,k])  for the rows r = offsets[e] .. offsets[e]+counts[e]-1 of expert e.
+ *   MOE_MX4_SWIGLU: the first N/2 features are the gate a, the others b: out[r,n] = bf16_rne(a/(1+exp(-a)) * b),
+ *   n < N/2, both in fp32.
+ *   x: codes and scales of [capacity, K]; w: of [E_local * N, K] (expert e's feature n is row e*N + n);
+ *   counts [E_local] and offsets (at least E_local) int32 on the device, as from moe_align_permute;
+ *   out [capacity, N] bf16 ([capacity, N/2] with the gate).  Rows of no expert (pads) are neither used nor written.
+ *   Products are exact, sums fp32 in the tensor cores.  A NaN block of a row makes that row NaN, of a weight row that
+ *   feature.  Deterministic.
+ *   An expert whose rows do not lie in [0, capacity) is skipped and MOE_ERR_BAD_ROW recorded in device_status (a
+ *   device int32 or NULL); the experts' row ranges must not overlap.
+ *   Errors: INVALID_ARG (sizes, N % 8 != 0 or N % 16 with the gate, K % 32, N or K beyond 2^20, null or misaligned
+ *   pointers), UNSUPPORTED (E_local > 1024).
+ */
+MOE_API moe_status_t moe_grouped_gemm_mx4(const void* x_codes, const void* x_scales, const void* w_codes,
+                                          const void* w_scales, const int32_t* counts, const int32_t* offsets,
+                                          int32_t E_local, int64_t capacity, int32_t N, int32_t K, uint32_t flags,
+                                          void* out, int32_t* device_status, void* stream);
 
 /*
  * Read the device status word (first 4 bytes of an align workspace, or any

@@ -32,6 +32,7 @@ MOE_GATHER_ZERO_PAD = 2
 MOE_GATHER_HIDDEN_READY = 4
 MOE_DISPATCH_GIVEN_IDS = 8
 MOE_SCORING_SIGMOID = 16
+MOE_MX4_SWIGLU = 32
 
 # Every symbol include/moe_route.h declares, with (restype, argtypes).
 _P, _I32, _I64, _U32, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32, ctypes.c_size_t
@@ -53,6 +54,13 @@ SIGNATURES = {
     "moe_route_dispatch": (ctypes.c_int, [_P, ctypes.c_int, _P, _I64, _I32, _I32, _I32, _U32, _P, _I32, _I32, _P, _P,
                                           _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "moe_reduce_partials": (ctypes.c_int, [_P, _I32, _I64, _I32, _P, _P]),
+    "moe_combine_backward": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _I64, _I32, _I32, _I64, _U32, _P, _P, _P, _P]),
+    "moe_gather_backward": (ctypes.c_int, [_P, _P, _I64, _I32, _I32, _I64, _P, _P, _P]),
+    "moe_topk_softmax_backward": (ctypes.c_int, [_P, _P, ctypes.c_int, _P, _P, _I64, _I32, _I32, _U32, _P, _P, _P]),
+    "moe_quantize_mx4": (ctypes.c_int, [_P, _I64, _I32, _P, _P, _P, _P]),
+    "moe_dequantize_mx4": (ctypes.c_int, [_P, _P, _I64, _I32, _P, _P]),
+    "moe_gather_mx4": (ctypes.c_int, [_P, _I64, _I32, _I32, _P, _I64, _P, _P, _P, _P]),
+    "moe_grouped_gemm_mx4": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _I32, _I64, _I32, _I32, _U32, _P, _P, _P]),
 }
 
 _lib: Optional[ctypes.CDLL] = None
@@ -365,3 +373,223 @@ def moe_read_status(device_status_word: torch.Tensor, stream=None) -> int:
     _check(load_library().moe_read_status(_dev(device_status_word, "device_status_word"), _stream(stream),
                                           ctypes.byref(v)), "moe_read_status")
     return int(v.value)
+
+
+# ------------------------------------------------------------ gradients and 4-bit products --
+def _arg(t, name: str, dtype, shape, device: torch.device, optional: bool = False):
+    """Pointer of a contiguous CUDA tensor of this dtype, shape and device (ValueError otherwise); None stays None."""
+    if t is None:
+        if optional:
+            return None
+        raise ValueError(f"{name} is missing")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (the routing path runs only on the GPU)")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _matrix(t, name: str, dtype=None):
+    if t is None or t.dim() != 2 or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{name} must be a matrix" + (f" of {dtype}" if dtype is not None else ""))
+    return t.shape
+
+
+def _call(name: str, device: torch.device, stream, *args) -> None:
+    """Run an entry point with `device` current, on `stream` or that device's current stream (the last argument)."""
+    if device.type != "cuda":
+        raise ValueError(f"{name} needs CUDA tensors (the routing path runs only on the GPU)")
+    if isinstance(stream, torch.cuda.Stream) and stream.device != device:
+        raise ValueError(f"{name}: the stream belongs to {stream.device}, the tensors to {device}")
+    fn = getattr(load_library(), name)
+    if torch.cuda.current_device() == device.index:
+        st = fn(*args, _stream(stream))
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, _stream(stream))
+    _check(st, name)
+
+
+def _slots(inv_perm, T: int, k: int, device) -> int:
+    return _arg(inv_perm, "inv_perm", torch.int32, (T * k,), device)
+
+
+def _status_arg(device_status, device):
+    """The status word: the first element of an int32 tensor (a workspace, or a word of its own)."""
+    if device_status is None:
+        return None
+    if device_status.numel() < 1:
+        raise ValueError("device_status must hold a word")
+    return _arg(device_status, "device_status", torch.int32, tuple(device_status.shape), device)
+
+
+def moe_combine_backward(grad_out: torch.Tensor, expert_out: torch.Tensor, topk_weights: torch.Tensor,
+                         inv_perm: torch.Tensor, grad_expert_out: Optional[torch.Tensor] = None,
+                         grad_topk_weights: Optional[torch.Tensor] = None,
+                         sorted_token_ids: Optional[torch.Tensor] = None,
+                         num_tokens_post_pad: Optional[torch.Tensor] = None, zero_pad: bool = False,
+                         device_status: Optional[torch.Tensor] = None, stream=None):
+    """Gradient of moe_combine: grad_out [T, H] bf16, expert_out [capacity, H] bf16 and topk_weights [T, k] fp32 ->
+    (grad_expert_out [capacity, H] bf16, grad_topk_weights [T, k] fp32).
+
+    zero_pad writes +0 into the pad rows below N_pad (needs sorted_token_ids and num_tokens_post_pad); other rows of
+    no slot are left as they were.  grad_expert_out may be expert_out itself."""
+    T, H = _matrix(grad_out, "grad_out")
+    k = _matrix(topk_weights, "topk_weights")[1]
+    capacity = _matrix(expert_out, "expert_out")[0]
+    dev, bf16 = grad_out.device, torch.bfloat16
+    if grad_expert_out is None:
+        grad_expert_out = torch.empty((capacity, H), dtype=bf16, device=dev)
+    if grad_topk_weights is None:
+        grad_topk_weights = torch.empty((T, k), dtype=torch.float32, device=dev)
+    pads = (None, None)
+    if zero_pad:
+        pads = (_arg(sorted_token_ids, "sorted_token_ids", torch.int32, (capacity,), dev),
+                _arg(num_tokens_post_pad, "num_tokens_post_pad", torch.int32, (1,), dev))
+    _call("moe_combine_backward", dev, stream, _arg(grad_out, "grad_out", bf16, (T, H), dev),
+          _arg(expert_out, "expert_out", bf16, (capacity, H), dev),
+          _arg(topk_weights, "topk_weights", torch.float32, (T, k), dev), _slots(inv_perm, T, k, dev), *pads, T, k, H,
+          capacity, MOE_GATHER_ZERO_PAD if zero_pad else 0,
+          _arg(grad_expert_out, "grad_expert_out", bf16, (capacity, H), dev),
+          _arg(grad_topk_weights, "grad_topk_weights", torch.float32, (T, k), dev), _status_arg(device_status, dev))
+    return grad_expert_out, grad_topk_weights
+
+
+def moe_gather_backward(grad_permuted: torch.Tensor, inv_perm: torch.Tensor, k: int,
+                        grad_hidden: Optional[torch.Tensor] = None, device_status: Optional[torch.Tensor] = None,
+                        stream=None) -> torch.Tensor:
+    """Gradient of moe_gather: grad_permuted [capacity, H] bf16 -> grad_hidden [T, H] bf16, each token's local rows
+    summed in fp32 (inv_perm holds T*k slots)."""
+    capacity, H = _matrix(grad_permuted, "grad_permuted")
+    if k < 1 or inv_perm.numel() % k != 0:
+        raise ValueError(f"inv_perm must hold T * k slots, got {inv_perm.numel()} with k = {k}")
+    T, dev = inv_perm.numel() // k, grad_permuted.device
+    if grad_hidden is None:
+        grad_hidden = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+    _call("moe_gather_backward", dev, stream,
+          _arg(grad_permuted, "grad_permuted", torch.bfloat16, (capacity, H), dev), _slots(inv_perm, T, k, dev), T, k, H,
+          capacity, _arg(grad_hidden, "grad_hidden", torch.bfloat16, (T, H), dev), _status_arg(device_status, dev))
+    return grad_hidden
+
+
+def moe_topk_softmax_backward(grad_topk_weights: torch.Tensor, logits: torch.Tensor, topk_weights: torch.Tensor,
+                              topk_ids: torch.Tensor, renormalize: bool, grad_logits: Optional[torch.Tensor] = None,
+                              device_status: Optional[torch.Tensor] = None, stream=None,
+                              scoring: str = "softmax") -> torch.Tensor:
+    """Gradient of moe_topk_softmax: grad_topk_weights [T, k] fp32 -> grad_logits [T, E] of the logits' dtype.
+    topk_weights and topk_ids are what moe_topk_softmax returned with the same renormalize and scoring."""
+    T, E = _matrix(logits, "logits")
+    k = _matrix(topk_weights, "topk_weights")[1]
+    dev, dtype = logits.device, logits.dtype
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"logits dtype {dtype} unsupported (bf16 or fp32)")
+    if grad_logits is None:
+        grad_logits = torch.empty((T, E), dtype=dtype, device=dev)
+    f32 = torch.float32
+    _call("moe_topk_softmax_backward", dev, stream, _arg(grad_topk_weights, "grad_topk_weights", f32, (T, k), dev),
+          _arg(logits, "logits", dtype, (T, E), dev), MOE_DTYPE_BF16 if dtype == torch.bfloat16 else MOE_DTYPE_F32,
+          _arg(topk_weights, "topk_weights", f32, (T, k), dev), _arg(topk_ids, "topk_ids", torch.int32, (T, k), dev), T,
+          E, k, (MOE_RENORMALIZE if renormalize else 0) | _scoring_flag(scoring),
+          _arg(grad_logits, "grad_logits", dtype, (T, E), dev), _status_arg(device_status, dev))
+    return grad_logits
+
+
+class Mx4Tensor(NamedTuple):
+    """A matrix [rows, K] in microscaled 4-bit floating point (layout: moe_route.h)."""
+    codes: torch.Tensor   # uint8 [rows, K/2]
+    scales: torch.Tensor  # uint8 [ceil(K/128), rows, 4]
+
+    @property
+    def rows(self) -> int:
+        return self.codes.shape[0]
+
+    @property
+    def K(self) -> int:
+        return self.codes.shape[1] * 2
+
+
+def alloc_mx4(rows: int, K: int, device) -> Mx4Tensor:
+    if K < 32 or K % 32 != 0:
+        raise ValueError(f"a row holds whole blocks of 32 elements, got K = {K}")
+    return Mx4Tensor(torch.empty((rows, K // 2), dtype=torch.uint8, device=device),
+                     torch.empty((-(-K // 128), rows, 4), dtype=torch.uint8, device=device))
+
+
+def _mx4_args(q: Mx4Tensor, name: str, device):
+    _matrix(q.codes, f"{name}.codes")
+    return (_arg(q.codes, f"{name}.codes", torch.uint8, (q.rows, q.K // 2), device),
+            _arg(q.scales, f"{name}.scales", torch.uint8, (-(-q.K // 128), q.rows, 4), device))
+
+
+def _mx4_out(out: Optional[Mx4Tensor], rows: int, K: int, device) -> Mx4Tensor:
+    if out is None:
+        return alloc_mx4(rows, K, device)
+    if (out.rows, out.K) != (rows, K):
+        raise ValueError(f"out holds [{out.rows}, {out.K}], [{rows}, {K}] is needed")
+    return out
+
+
+def moe_quantize_mx4(x: torch.Tensor, out: Optional[Mx4Tensor] = None, num_rows: Optional[torch.Tensor] = None,
+                     stream=None) -> Mx4Tensor:
+    """x [rows, K] bf16 -> microscaled 4-bit floating point (K a multiple of 32).  num_rows (int32 [1] on the device):
+    rows from there on are neither read nor written."""
+    rows, K = _matrix(x, "x")
+    out = _mx4_out(out, rows, K, x.device)
+    _call("moe_quantize_mx4", x.device, stream, _arg(x, "x", torch.bfloat16, (rows, K), x.device), rows, K,
+          _arg(num_rows, "num_rows", torch.int32, (1,), x.device, optional=True),
+          *_mx4_args(out, "out", x.device))
+    return out
+
+
+def moe_dequantize_mx4(q: Mx4Tensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The values of q as bf16 [rows, K]."""
+    dev = q.codes.device
+    if out is None:
+        out = torch.empty((q.rows, q.K), dtype=torch.bfloat16, device=dev)
+    _call("moe_dequantize_mx4", dev, stream, *_mx4_args(q, "q", dev), q.rows, q.K,
+          _arg(out, "out", torch.bfloat16, (q.rows, q.K), dev))
+    return out
+
+
+def moe_gather_mx4(hidden: torch.Tensor, k: int, inv_perm: torch.Tensor, capacity: int,
+                   out: Optional[Mx4Tensor] = None, device_status: Optional[torch.Tensor] = None,
+                   stream=None) -> Mx4Tensor:
+    """moe_gather in microscaled 4-bit floating point: hidden [T, H] bf16 -> expert-grouped rows [capacity, H].
+    Rows of no slot are left as they were."""
+    T, H = _matrix(hidden, "hidden")
+    dev = hidden.device
+    out = _mx4_out(out, capacity, H, dev)
+    _call("moe_gather_mx4", dev, stream, _arg(hidden, "hidden", torch.bfloat16, (T, H), dev), T, H, k,
+          _slots(inv_perm, T, k, dev), capacity, *_mx4_args(out, "out", dev), _status_arg(device_status, dev))
+    return out
+
+
+def moe_grouped_gemm_mx4(x: Mx4Tensor, w: Mx4Tensor, counts: torch.Tensor, offsets: torch.Tensor,
+                         out: Optional[torch.Tensor] = None, swiglu: bool = False,
+                         device_status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The experts' product on expert-grouped rows: x [capacity, K], w [E_local * N, K] (expert e's feature n in row
+    e * N + n), counts [E_local] and offsets [E_local + 1] as from moe_align_permute -> out [capacity, N] bf16, or
+    [capacity, N/2] = silu(first half) * second half with swiglu.  Rows of no expert are left as they were."""
+    dev = x.codes.device
+    E, capacity, K = counts.numel(), x.rows, x.K
+    if E < 1 or w.rows % E != 0:
+        raise ValueError(f"w must hold E_local * N rows, got {w.rows} for {E} experts")
+    if w.K != K:
+        raise ValueError(f"x has rows of {K}, w of {w.K}")
+    N = w.rows // E
+    if swiglu and N % 2 != 0:
+        raise ValueError(f"swiglu needs an even number of features, got {N}")
+    cols = N // 2 if swiglu else N
+    if out is None:
+        out = torch.empty((capacity, cols), dtype=torch.bfloat16, device=dev)
+    _call("moe_grouped_gemm_mx4", dev, stream, *_mx4_args(x, "x", dev), *_mx4_args(w, "w", dev),
+          _arg(counts, "counts", torch.int32, (E,), dev), _arg(offsets, "offsets", torch.int32, (E + 1,), dev), E,
+          capacity, N, K, MOE_MX4_SWIGLU if swiglu else 0, _arg(out, "out", torch.bfloat16, (capacity, cols), dev),
+          _status_arg(device_status, dev))
+    return out

@@ -1,0 +1,212 @@
+// mx4_cast.cu -- rows to microscaled 4-bit floating point and back, and the permute-gather in that format.
+//
+// Format (the OCP Microscaling Formats specification v1.0, MXFP4): 32 consecutive elements of a row share one
+// power-of-two scale 2^s, kept as the byte s + 127 (E8M0); an element is an E2M1 code c (sign, two exponent bits,
+// one mantissa bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6) and stands for c 2^s.
+//   s = clamp(floor(log2(max |x|)) - 2, -127, 127), c = x 2^-s to nearest, ties to the even code, beyond 6 to 6.
+// 2^-s is exact and x 2^-s is exact in fp32 (or below the smallest code's half), so each element is rounded once.
+// A block that holds an infinity or a NaN gets the scale byte 255, which stands for NaN, and zero codes: the block
+// reads back as NaN.  A block of zeros gets scale byte 0.
+//
+// Layout: codes [rows, K/2], the even element in the low half of the byte; scales [ceil(K/128), rows, 4]: the bytes
+// of the four blocks of a 128-element chunk side by side, rows next to each other, which is how the product's tiles
+// read them (32 lanes, 128 bytes).  Blocks past K in the last chunk hold 127 (a scale of 1).
+//
+// All three kernels are bandwidth-bound: 2 K bytes a row on the wide side, 17/32 K on the narrow one.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "common.cuh"
+
+namespace {
+
+constexpr int kCastThreads = 256;
+
+// Eight bf16 of a lane (four lanes hold a block): the block's scale byte and the lane's eight codes.
+__device__ __forceinline__ uint32_t quantize8(const uint4& v, uint32_t& scale_byte) {
+  const uint32_t a0 = v.x & 0x7fff7fffu, a1 = v.y & 0x7fff7fffu, a2 = v.z & 0x7fff7fffu, a3 = v.w & 0x7fff7fffu;
+  uint32_t m = __vmaxu2(__vmaxu2(a0, a1), __vmaxu2(a2, a3));  // magnitudes order as integers, NaN above infinity
+  m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  const uint32_t top = max(m & 0xffffu, m >> 16);
+  const uint32_t field = top >> 7;  // biased exponent: floor(log2) + 127 where normal; s + 127 = field - 2, at least 0
+  if (field == 255u) {
+    scale_byte = 255u;
+    return 0u;
+  }
+  scale_byte = field > 2u ? field - 2u : 0u;
+  const float f = __uint_as_float((254u - scale_byte) << 23);  // 2^-s, normal: the byte is at most 252
+  uint32_t codes;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+      : "=r"(codes)
+      : "f"(moe::bf16_lo(v.x) * f), "f"(moe::bf16_hi(v.x) * f), "f"(moe::bf16_lo(v.y) * f),
+        "f"(moe::bf16_hi(v.y) * f), "f"(moe::bf16_lo(v.z) * f), "f"(moe::bf16_hi(v.z) * f),
+        "f"(moe::bf16_lo(v.w) * f), "f"(moe::bf16_hi(v.w) * f));
+  return codes;
+}
+
+// Scale byte of the lane's block, gathered over 16 lanes (four blocks, one chunk) into the chunk's word.
+__device__ __forceinline__ uint32_t chunk_word(uint32_t scale_byte, bool in_range) {
+  uint32_t b = in_range ? scale_byte : 127u;
+  b |= __shfl_down_sync(0xffffffffu, b, 4) << 8;    // lanes 0, 8 of the 16 hold blocks (0,1), (2,3)
+  b = (b & 0xffffu) | (__shfl_down_sync(0xffffffffu, b, 8) << 16);
+  return b;  // valid in lanes 0 and 16
+}
+
+// One thread per eight elements; a warp takes 256 consecutive elements (two chunks) of a row.
+__global__ void __launch_bounds__(kCastThreads)
+quantize_kernel(const uint4* __restrict__ x, int64_t rows, const int32_t* __restrict__ num_rows, int nv, int segs,
+                uint32_t* __restrict__ codes, uint32_t* __restrict__ scales) {
+  moe::pdl_launch_dependents();
+  moe::pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t wid = (static_cast<int64_t>(blockIdx.x) * kCastThreads + threadIdx.x) >> 5;
+  const int64_t row = wid / segs;
+  if (row >= rows || (num_rows != nullptr && row >= num_rows[0])) return;
+  const int v = static_cast<int>(wid - row * segs) * 32 + lane;
+  const bool in = v < nv;
+  uint32_t sb;
+  const uint32_t c = quantize8(in ? moe::ld_stream(x + row * nv + v) : make_uint4(0u, 0u, 0u, 0u), sb);
+  const uint32_t word = chunk_word(sb, in);
+  if (in) codes[row * nv + v] = c;
+  if ((lane & 15) == 0 && in) scales[static_cast<int64_t>(v >> 4) * rows + row] = word;
+}
+
+// The permute-gather: a token's row is read and quantised once and written to each of its local rows.
+__global__ void __launch_bounds__(kCastThreads)
+gather_mx4_kernel(const uint4* __restrict__ x, int64_t T, int nv, int segs, int k,
+                  const int32_t* __restrict__ inv_perm, int64_t capacity, uint32_t* __restrict__ codes,
+                  uint32_t* __restrict__ scales, int32_t* status) {
+  moe::pdl_launch_dependents();
+  moe::pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t wid = (static_cast<int64_t>(blockIdx.x) * kCastThreads + threadIdx.x) >> 5;
+  const int64_t t = wid / segs;
+  if (t >= T) return;
+  int r = -1;
+  if (lane < k) {
+    r = inv_perm[t * k + lane];
+    if (r < -1 || static_cast<int64_t>(r) >= capacity) {
+      moe::record_status(status, MOE_ERR_BAD_ROW);
+      r = -1;
+    }
+  }
+  unsigned local = __ballot_sync(0xffffffffu, r >= 0);
+  if (local == 0u) return;  // no local slot: the row is not read
+  const int v = static_cast<int>(wid - t * segs) * 32 + lane;
+  const bool in = v < nv;
+  uint32_t sb;
+  const uint32_t c = quantize8(in ? moe::ld_stream(x + t * nv + v) : make_uint4(0u, 0u, 0u, 0u), sb);
+  const uint32_t word = chunk_word(sb, in);
+  while (local != 0u) {
+    const int64_t dst = __shfl_sync(0xffffffffu, r, __ffs(local) - 1);
+    local &= local - 1u;
+    if (in) codes[dst * nv + v] = c;
+    if ((lane & 15) == 0 && in) scales[static_cast<int64_t>(v >> 4) * capacity + dst] = word;
+  }
+}
+
+// Eight codes and their scale byte -> eight bf16 (exact where the value is representable).
+__global__ void __launch_bounds__(kCastThreads)
+dequantize_kernel(const uint32_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t rows, int nv,
+                  int segs, uint4* __restrict__ out) {
+  moe::pdl_launch_dependents();
+  moe::pdl_wait();
+  const int64_t wid = (static_cast<int64_t>(blockIdx.x) * kCastThreads + threadIdx.x) >> 5;
+  const int64_t row = wid / segs;
+  if (row >= rows) return;
+  const int v = static_cast<int>(wid - row * segs) * 32 + (threadIdx.x & 31);
+  if (v >= nv) return;
+  const uint32_t c = codes[row * nv + v];
+  const uint32_t byte = scales[(static_cast<int64_t>(v >> 4) * rows + row) * 4 + ((v >> 2) & 3)];
+  // 2^(byte - 127): below a byte of 1 a subnormal, 255 NaN
+  const float f = byte == 255u ? __uint_as_float(0x7fc00000u)
+                               : byte == 0u ? __uint_as_float(0x00400000u) : __uint_as_float(byte << 23);
+  uint32_t h[4];
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(c));
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, u;\n\t}"
+        : "=f"(lo), "=f"(hi)
+        : "r"(h[i]));
+    o[i] = moe::pack_bf16x2(lo * f, hi * f);
+  }
+  moe::st_stream(out + row * nv + v, make_uint4(o[0], o[1], o[2], o[3]));
+}
+
+// Sizes of a matrix in the format: K in blocks of 32, and every element index below 2^47.
+bool mx4_sizes_ok(int64_t rows, int32_t K) {
+  return rows >= 0 && rows < (int64_t{1} << 31) && K >= 32 && (K % 32) == 0 && K <= (1 << 20);
+}
+
+bool cast_grid(int64_t rows, int segs, unsigned* grid) {
+  const int64_t blocks = (rows * segs + kCastThreads / 32 - 1) / (kCastThreads / 32);
+  *grid = static_cast<unsigned>(blocks);
+  return blocks <= 0x7fffffff;
+}
+
+}  // namespace
+
+extern "C" moe_status_t moe_quantize_mx4(const void* x, int64_t rows, int32_t K, const int32_t* num_rows,
+                                         void* codes, void* scales, void* stream) {
+  if (!mx4_sizes_ok(rows, K)) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  if (x == nullptr || codes == nullptr || scales == nullptr) return MOE_ERR_INVALID_ARG;
+  if (!moe_host::aligned16(x) || !moe_host::aligned16(codes) || !moe_host::aligned16(scales))
+    return MOE_ERR_INVALID_ARG;
+  const int nv = K / 8, segs = (nv + 31) / 32;
+  unsigned grid;
+  if (!cast_grid(rows, segs, &grid)) return MOE_ERR_UNSUPPORTED;
+  return moe_host::launch_pdl(quantize_kernel, dim3(grid), dim3(kCastThreads), 0, static_cast<cudaStream_t>(stream),
+                              static_cast<const uint4*>(x), rows, num_rows, nv, segs, static_cast<uint32_t*>(codes),
+                              static_cast<uint32_t*>(scales));
+}
+
+extern "C" moe_status_t moe_dequantize_mx4(const void* codes, const void* scales, int64_t rows, int32_t K, void* out,
+                                           void* stream) {
+  if (!mx4_sizes_ok(rows, K)) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  if (out == nullptr || codes == nullptr || scales == nullptr) return MOE_ERR_INVALID_ARG;
+  if (!moe_host::aligned16(out) || !moe_host::aligned16(codes) || !moe_host::aligned16(scales))
+    return MOE_ERR_INVALID_ARG;
+  const int nv = K / 8, segs = (nv + 31) / 32;
+  unsigned grid;
+  if (!cast_grid(rows, segs, &grid)) return MOE_ERR_UNSUPPORTED;
+  return moe_host::launch_pdl(dequantize_kernel, dim3(grid), dim3(kCastThreads), 0,
+                              static_cast<cudaStream_t>(stream), static_cast<const uint32_t*>(codes),
+                              static_cast<const uint8_t*>(scales), rows, nv, segs, static_cast<uint4*>(out));
+}
+
+extern "C" moe_status_t moe_gather_mx4(const void* hidden, int64_t T, int32_t H, int32_t k, const int32_t* inv_perm,
+                                       int64_t capacity, void* codes, void* scales, int32_t* device_status,
+                                       void* stream) {
+  if (T < 0 || k < 1 || !mx4_sizes_ok(capacity, H)) return MOE_ERR_INVALID_ARG;
+  if (k > 32) return MOE_ERR_UNSUPPORTED;
+  if (T > (int64_t{1} << 40) || T * k >= (int64_t{1} << 30)) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (hidden == nullptr || inv_perm == nullptr) return MOE_ERR_INVALID_ARG;
+  if (capacity > 0 && (codes == nullptr || scales == nullptr)) return MOE_ERR_INVALID_ARG;
+  if (!moe_host::aligned16(hidden) || !moe_host::aligned16(codes) || !moe_host::aligned16(scales))
+    return MOE_ERR_INVALID_ARG;
+  const int nv = H / 8, segs = (nv + 31) / 32;
+  unsigned grid;
+  if (!cast_grid(T, segs, &grid)) return MOE_ERR_UNSUPPORTED;
+  return moe_host::launch_pdl(gather_mx4_kernel, dim3(grid), dim3(kCastThreads), 0, static_cast<cudaStream_t>(stream),
+                              static_cast<const uint4*>(hidden), T, nv, segs, static_cast<int>(k), inv_perm, capacity,
+                              static_cast<uint32_t*>(codes), static_cast<uint32_t*>(scales), device_status);
+}

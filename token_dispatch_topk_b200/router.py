@@ -20,7 +20,8 @@ from . import binding as B
 class MoeRouter:
     def __init__(self, T: int, E: int, k: int, H: int, block_size: int, renormalize: bool,
                  E_local: Optional[int] = None, expert_map: Optional[torch.Tensor] = None,
-                 logits_dtype: torch.dtype = torch.bfloat16, device="cuda", scoring: str = "softmax"):
+                 logits_dtype: torch.dtype = torch.bfloat16, device="cuda", scoring: str = "softmax",
+                 training: bool = False):
         B.load_library()
         self.scoring = scoring
         self.T, self.E, self.k, self.H, self.block_size = T, E, k, H, block_size
@@ -40,6 +41,13 @@ class MoeRouter:
         # device-side inputs for the end-to-end path
         self.logits_dev = torch.empty((T, E), dtype=logits_dtype, device=self.device)
         self.hidden_dev = torch.empty((T, H), dtype=torch.bfloat16, device=self.device)
+        # gradients (training): of the expert outputs, the combine weights, the hidden rows and the logits
+        self.training = training
+        if training:
+            self.grad_expert_out = torch.zeros((self.capacity, H), dtype=torch.bfloat16, device=self.device)
+            self.grad_topk_weights = torch.empty((T, k), dtype=torch.float32, device=self.device)
+            self.grad_hidden = torch.empty((T, H), dtype=torch.bfloat16, device=self.device)
+            self.grad_logits = torch.empty((T, E), dtype=logits_dtype, device=self.device)
 
     # ------------------------------------------------------------------ stages --
     def gate(self, logits: torch.Tensor, stream=None):
@@ -60,6 +68,37 @@ class MoeRouter:
         w = self.topk_weights if topk_weights is None else topk_weights
         return B.moe_combine(expert_out, w, self.align.inv_perm, self.out, device_status=self.workspace,
                              stream=stream)
+
+    # ----------------------------------------------------------------- gradients --
+    def _needs_training(self) -> None:
+        if not self.training:
+            raise RuntimeError("this MoeRouter has no gradient buffers: construct it with training=True")
+
+    def combine_backward(self, grad_out: torch.Tensor, expert_out: torch.Tensor,
+                         topk_weights: Optional[torch.Tensor] = None, stream=None):
+        """The combine's gradients for the step's routes: (grad_expert_out, grad_topk_weights), both this router's
+        buffers.  The pad rows of grad_expert_out below N_pad are +0, so products over whole blocks may use it."""
+        self._needs_training()
+        w = self.topk_weights if topk_weights is None else topk_weights
+        return B.moe_combine_backward(grad_out, expert_out, w, self.align.inv_perm, self.grad_expert_out,
+                                      self.grad_topk_weights, self.align.sorted_token_ids,
+                                      self.align.num_tokens_post_pad, zero_pad=True, device_status=self.workspace,
+                                      stream=stream)
+
+    def gather_backward(self, grad_permuted: torch.Tensor, stream=None) -> torch.Tensor:
+        """The permute-gather's gradient: grad_hidden, this router's buffer."""
+        self._needs_training()
+        return B.moe_gather_backward(grad_permuted, self.align.inv_perm, self.k, self.grad_hidden,
+                                     device_status=self.workspace, stream=stream)
+
+    def gate_backward(self, logits: torch.Tensor, grad_topk_weights: Optional[torch.Tensor] = None,
+                      stream=None) -> torch.Tensor:
+        """The gating's gradient, by default from combine_backward's weights: grad_logits, this router's buffer."""
+        self._needs_training()
+        g = self.grad_topk_weights if grad_topk_weights is None else grad_topk_weights
+        return B.moe_topk_softmax_backward(g, logits, self.topk_weights, self.topk_ids, self.renormalize,
+                                           self.grad_logits, device_status=self.workspace, stream=stream,
+                                           scoring=self.scoring)
 
     def dispatch(self, logits: Optional[torch.Tensor], hidden: torch.Tensor, stream=None,
                  topk_ids: Optional[torch.Tensor] = None):
@@ -103,6 +142,13 @@ class MoeRouter:
         """The step for routes chosen by the caller (no gating): align + permute-gather + combine."""
         self.dispatch(None, hidden, stream, topk_ids=topk_ids)
         return self.combine(expert_out, topk_weights, stream=stream)
+
+    def step_mx4(self, logits: torch.Tensor, hidden: torch.Tensor, experts, stream=None) -> torch.Tensor:
+        """The whole layer with the experts in microscaled 4-bit floating point (experts.Mx4Experts): gate + align +
+        quantising permute-gather + gated product + product + combine."""
+        self.gate(logits, stream)
+        self.align_permute(stream=stream)
+        return self.combine(experts.forward(hidden, self.k, self.align, self.workspace, stream), stream=stream)
 
     def step_from_host(self, logits_host: torch.Tensor, hidden_host: torch.Tensor, expert_out: torch.Tensor,
                        out_host: torch.Tensor, stream=None) -> torch.Tensor:
