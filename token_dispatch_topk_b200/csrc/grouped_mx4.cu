@@ -5,15 +5,21 @@
 //   out[r, n] = bf16( silu(a) b ), a = sum_k x[r, k] w[e, n, k], b = sum_k x[r, k] w[e, N/2 + n, k], n < N/2,
 // silu(a) = a / (1 + exp(-a)), sums and gate in fp32, one rounding.
 //
-// A tile is 128 features of one expert (the 128 TMEM lanes, operand A = weights) by up to kTileT of its rows
-// (operand B, the accumulator's columns).  Features, not rows, take the fixed side of 128: an expert has any number
-// of rows, one at decode, and the column side of tcgen05.mma goes in steps of 16.  With the gate a tile's lanes are
-// 64 gate and the 64 matching up features.  The rows of an expert are split evenly over as few tiles as hold them.
+// A tile is features of one expert (operand A = weights, the 128 TMEM lanes of a CTA) by up to kTileT of its rows
+// (operand B, the accumulator's columns).  Features, not rows, take the fixed side: an expert has any number of rows,
+// one at decode, and the column side of tcgen05.mma goes in steps of 16 or 32.  With the gate a warp's 32 lanes are 16
+// gate and the 16 matching up features, so that one thread holds both.  The rows of an expert are split evenly over as
+// few tiles as hold them.
 //
-// One CTA per SM walks the tiles.  Warp 0: TMA loads into a ring of 256-element stages.  Warps 2 and 3: the scale
-// words of the stage's two 128-element chunks into the order tcgen05.cp wants, read ahead into registers.
-// Warp 1: copies the scales to TMEM and issues the products (kind::mxf4, block-scaled, 64 elements each).  Warps
-// 4..7: the accumulator of the previous tile out of TMEM, through shared memory, to rows of out.
+// Two forms (Shape<1>, Shape<2>): for few rows an expert, one CTA a tile, 128 features by up to 64 rows, a deep ring of
+// stages; for many, a pair of CTAs a tile (cta_group::2), 256 features by up to 224 rows, each CTA loading its own
+// 128 features and half of the rows, which halves what comes through L2 per product.
+//
+// The CTAs (one per SM) walk the tiles.  Warp 0: TMA loads into a ring of 256-element stages.  Warps 2 and 3: the
+// scale words of the stage's two 128-element chunks into the order tcgen05.cp wants, read ahead into registers.
+// Warp 1: copies the scales to TMEM and issues the products (kind::mxf4, block-scaled, 64 elements each; in a pair the
+// second CTA's warp 1 only tells the first that its stage is there).  Warps 4..11: the accumulator of the previous tile
+// out of TMEM, each warp its 32 lanes by every other 32 columns, transposed by stmatrix into rows of out.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -23,40 +29,47 @@
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kTileF = 128;             // features a tile
-constexpr int kTileT = 128;             // rows a tile, at most
+constexpr int kThreads = 384;
+constexpr int kEpiWarps = 8;
+constexpr int kTileF = 128;             // features a CTA and tile
 constexpr int kStageK = 256;            // elements of K a stage: 128 bytes, one swizzle atom
-constexpr int kStages = 6;
-constexpr int kBoxT = 32;               // rows of x a TMA box
-constexpr int kBoxF = 64;               // features a TMA box (the gate and up halves of a tile)
+constexpr int kBoxRows = 16;            // rows of x a TMA box; of the weights with the gate (16 gate, 16 up, ...)
 constexpr int kBytesA = kTileF * kStageK / 2;
-constexpr int kBytesB = kTileT * kStageK / 2;
 constexpr int kAtom = 512;              // scales of 128 rows by 128 elements
-constexpr int kBytesSf = 2 * kAtom + 2 * kAtom * (kTileT / 128);
-constexpr int kStageBytes = kBytesA + kBytesB;
-constexpr int kEpiT = 32;               // rows of a tile that go through shared memory at a time
-constexpr int kEpiStride = kTileF + 4;  // fp32 words a row there
+constexpr int kEpiT = 32;               // columns an epilogue warp takes at a time
+constexpr int kEpiStride = 32 + 8;      // bf16 a row of its transposed block (80 bytes: conflict-free)
 constexpr int kMaxExperts = 1024;
 constexpr int kSfAhead = 4;             // stages whose scales are in registers
-// TMEM columns: two accumulators, then each stage's scales (four columns an atom)
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kTmemSf = 2 * kTileT;
-constexpr uint32_t kTmemSfStage = 8 + 8 * (kTileT / 128);
-static_assert(kTmemSf + kStages * kTmemSfStage <= kTmemCols, "TMEM columns");
 
-struct __align__(1024) Smem {
-  uint8_t ab[kStages][kStageBytes];  // A then B, 128-byte swizzled
-  uint8_t sf[kStages][kBytesSf];     // A's two atoms, then B's
-  float epi[kEpiT * kEpiStride];
-  int32_t first_tile[kMaxExperts + 1];  // row tiles before expert e
-  int32_t warp_sums[8];
-  uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drained;
-  uint32_t tmem;
-  int abort;
-  int epi_go;
+template <int CG>  // CTAs a tile
+struct Shape {
+  static constexpr int kTileT = CG == 1 ? 64 : 224;  // rows a tile, at most
+  static constexpr int kStepT = CG == 1 ? 16 : 32;   // columns of a product: a multiple of this
+  static constexpr int kStages = CG == 1 ? 7 : 6;
+  static constexpr int kRowsB = kTileT / CG;         // rows of x a CTA loads
+  static constexpr int kBytesB = kRowsB * kStageK / 2;
+  static constexpr int kStageBytes = kBytesA + kBytesB;
+  static constexpr int kAtomsB = (kTileT + 127) / 128;
+  static constexpr int kBytesSf = 2 * kAtom * (1 + kAtomsB);
+  // TMEM columns: two accumulators, then two sets of a stage's scales (four columns an atom)
+  static constexpr uint32_t kSfCols = 8 + 8 * kAtomsB;
+  static constexpr uint32_t kTmemSf = 2 * kTileT;
+  static_assert(kTmemSf + 2 * kSfCols <= kTmemCols, "TMEM columns");
+  static_assert(kStageBytes % 1024 == 0 && kRowsB % kBoxRows == 0, "swizzle atoms");
+
+  struct __align__(1024) Smem {
+    uint8_t ab[kStages][kStageBytes];  // A then B, 128-byte swizzled
+    uint8_t sf[kStages][kBytesSf];     // A's two atoms, then B's, chunk by chunk
+    __nv_bfloat16 epi[kEpiWarps][kEpiT * kEpiStride];
+    int32_t first_tile[kMaxExperts + 1];  // row tiles before expert e
+    int32_t warp_sums[kThreads / 32];
+    uint64_t full[kStages], peer_full[kStages], empty[kStages], acc_full[2], acc_empty[2], drained;
+    uint32_t tmem;
+    int abort;
+  };
+  static_assert(sizeof(Smem) + 1024 <= 232448, "shared memory");
 };
-static_assert(sizeof(Smem) + 1024 <= 232448, "shared memory");
 
 struct ProductArgs {
   const uint32_t* x_sf;  // [chunks, capacity] scale words
@@ -66,7 +79,7 @@ struct ProductArgs {
   int E, N, K;
   int chunks;     // ceil(K / 128)
   int kstages;    // ceil(K / 256)
-  int ftiles;     // feature tiles
+  int ftiles;     // feature tiles (of a CTA, or of a pair)
   int gate;       // 1: silu(gate) * up
   int64_t capacity;
   __nv_bfloat16* out;
@@ -91,48 +104,104 @@ __device__ __forceinline__ uint64_t desc_plain(uint32_t addr) {
          (uint64_t{1} << 46);
 }
 
+// 512 bytes of scales to four TMEM columns; in a pair, each CTA's own shared memory to its own TMEM.
+template <int CG>
 __device__ __forceinline__ void sf_to_tmem(uint32_t taddr, uint32_t smem) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc_plain(smem)) : "memory");
+  if constexpr (CG == 1)
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc_plain(smem)) : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc_plain(smem)) : "memory");
 }
 
+template <int CG>
 __device__ __forceinline__ void mma_mx4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
                                         bool accumulate) {
+  if constexpr (CG == 1)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate ? 1u : 0u)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate ? 1u : 0u)
+        : "memory");
+}
+
+// Arrive at the barrier (in a pair: at both CTAs') once the tensor operations issued so far are done.
+template <int CG>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  if constexpr (CG == 1)
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                     moe::smem_addr(bar))
+                 : "memory");
+  else
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            moe::smem_addr(bar)),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+}
+
+// Arrive at CTA 0's barrier of the pair.
+__device__ __forceinline__ void arrive_first(uint64_t* bar) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate ? 1u : 0u)
+      "{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %0, 0;\n\t"
+      "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [r];\n\t}" ::"r"(moe::smem_addr(bar))
       : "memory");
 }
 
-__device__ __forceinline__ void commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(moe::smem_addr(bar))
-               : "memory");
+__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(moe::smem_addr(bar)), "r"(parity)
+      : "memory");
+  return done != 0u;
 }
 __device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
+// 16 lanes by 32 columns: thread t gets, for columns 8i + 2 (t % 4) + {0, 1}, v[4i + {0, 1}] of lane t / 4 and
+// v[4i + {2, 3}] of lane t / 4 + 8.
+__device__ __forceinline__ void tmem_ld16x32(uint32_t taddr, uint32_t (&v)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
       : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
-        "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
-        "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
       : "r"(taddr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// Four 8x8 blocks of bf16, transposed: lane 8m + j gives the address of row j of block m.
+__device__ __forceinline__ void stmatrix_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
+               "r"(c), "r"(d)
+               : "memory");
+}
+
+__device__ __forceinline__ float silu_times(uint32_t gate, uint32_t up) {
+  const float g = __uint_as_float(gate);
+  return __fdividef(g, 1.f + __expf(-g)) * __uint_as_float(up);
 }
 
 // A bounded wait that polls without sleeping (the wait itself suspends in hardware); it also gives up when another
 // role of the CTA has.
+template <bool kCluster = false>
 __device__ __forceinline__ bool wait_stage(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* status) {
-  if (moe::mbar_try_wait(bar, parity)) return true;
+  auto poll = [&] { return kCluster ? try_wait_cluster(bar, parity) : moe::mbar_try_wait(bar, parity); };
+  if (poll()) return true;
   const uint64_t t0 = moe::global_ns();
   for (;;) {
 #pragma unroll 1
     for (int i = 0; i < 64; ++i)
-      if (moe::mbar_try_wait(bar, parity)) return true;
+      if (poll()) return true;
     if (*abort != 0) return false;
     if (moe::global_ns() - t0 > moe::kWaitLimitNs) {
       moe::record_status(status, MOE_ERR_TIMEOUT);
@@ -142,82 +211,102 @@ __device__ __forceinline__ bool wait_stage(uint64_t* bar, uint32_t parity, volat
   }
 }
 
-// The tiles of this CTA, in order: expert by expert, then row tiles, features fastest.
+// The tiles of this CTA (or pair), in order: expert by expert, then row tiles, features fastest.
+template <int CG>
 struct Tiles {
   const ProductArgs& a;
   const int32_t* first;  // row tiles before expert e
   int64_t t, end;
   int e = 0;
-  int f, row0, rows;  // feature tile, first row, rows
+  int f, row0, rows;  // this CTA's feature tile, the tile's first row, its rows
 
   __device__ Tiles(const ProductArgs& args, const int32_t* first_tile)
-      : a(args), first(first_tile), t(static_cast<int64_t>(blockIdx.x) - gridDim.x),
+      : a(args), first(first_tile), t(static_cast<int64_t>(blockIdx.x / CG) - gridDim.x / CG),
         end(static_cast<int64_t>(first_tile[args.E]) * args.ftiles) {}
   __device__ bool next() {
-    t += gridDim.x;
+    t += gridDim.x / CG;
     if (t >= end) return false;
     const int rt = static_cast<int>(t / a.ftiles);
-    f = static_cast<int>(t - static_cast<int64_t>(rt) * a.ftiles);
+    f = static_cast<int>(t - static_cast<int64_t>(rt) * a.ftiles) * CG + (CG == 1 ? 0 : blockIdx.x % CG);
     while (first[e + 1] <= rt) ++e;
     const int cnt = a.counts[e], n = first[e + 1] - first[e];
-    const int per = ((cnt + n - 1) / n + 15) & ~15;  // at most kTileT
+    constexpr int kStep = Shape<CG>::kStepT;
+    const int per = ((cnt + n - 1) / n + kStep - 1) / kStep * kStep;  // at most kTileT
     const int i = rt - first[e];
     row0 = a.offsets[e] + i * per;
     rows = cnt - i * per < per ? cnt - i * per : per;
     return true;
   }
-  __device__ int cols() const { return (rows + 15) & ~15; }  // the product's columns
+  // the product's columns
+  __device__ int cols() const { return (rows + Shape<CG>::kStepT - 1) / Shape<CG>::kStepT * Shape<CG>::kStepT; }
+  // the first weight row of the tile (with the gate: of its gate features)
+  __device__ int64_t weight_row0() const {
+    return static_cast<int64_t>(e) * a.N + static_cast<int64_t>(f) * (a.gate ? kTileF / 2 : kTileF);
+  }
   // row of the weights that lane m of the tile holds (clamped: lanes past the expert's features are not stored)
-  __device__ int weight_row(int m) const {
-    const int64_t base = static_cast<int64_t>(e) * a.N;
-    const int64_t r = !a.gate ? base + f * kTileF + m
-                              : base + f * kBoxF + (m < kBoxF ? m : a.N / 2 + m - kBoxF);
+  __device__ int64_t weight_row(int m) const {
+    const int64_t r = weight_row0() + (!a.gate ? m : (m & 16 ? a.N / 2 : 0) + (m >> 5) * 16 + (m & 15));
     const int64_t last = static_cast<int64_t>(a.E) * a.N - 1;
-    return static_cast<int>(r < last ? r : last);
+    return r < last ? r : last;
   }
 };
 
+template <int CG>
 __global__ void __launch_bounds__(kThreads, 1)
 grouped_mx4_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                    const ProductArgs a) {
+  using S = Shape<CG>;
+  constexpr int kStages = S::kStages;
   extern __shared__ uint8_t smem_raw[];
-  Smem& s = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  typename S::Smem& s =
+      *reinterpret_cast<typename S::Smem*>(smem_raw + ((1024u - (moe::smem_addr(smem_raw) & 1023u)) & 1023u));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = CG == 1 ? 0 : blockIdx.x % CG;  // in the pair
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
       moe::mbar_init(&s.full[i], 3);  // the TMA warp and the two scale warps
+      moe::mbar_init(&s.peer_full[i], 1);
       moe::mbar_init(&s.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       moe::mbar_init(&s.acc_full[i], 1);
-      moe::mbar_init(&s.acc_empty[i], 4);
+      moe::mbar_init(&s.acc_empty[i], CG * kEpiWarps);
     }
     moe::mbar_init(&s.drained, 1);
     s.abort = 0;
     moe::fence_barrier_init();
   }
   if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(moe::smem_addr(&s.tmem)),
-                 "r"(kTmemCols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    if constexpr (CG == 1) {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(moe::smem_addr(&s.tmem)),
+                   "r"(kTmemCols)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(moe::smem_addr(&s.tmem)),
+                   "r"(kTmemCols)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
   }
   moe::pdl_launch_dependents();
   moe::pdl_wait();  // rows, scales, counts and offsets may come from the previous kernel
 
   // row tiles before each expert: four experts a thread
   {
-    int n[4], sum = 0;
+    constexpr int kPer = 4;
+    static_assert(kPer * 256 >= kMaxExperts, "experts a thread");
+    int n[kPer], sum = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int e = tid * 4 + i;
+    for (int i = 0; i < kPer; ++i) {
+      const int e = tid * kPer + i;
       n[i] = 0;
       if (e < a.E) {
         const int64_t cnt = a.counts[e], off = a.offsets[e];
         if (cnt < 0 || off < 0 || off + cnt > a.capacity)
           moe::record_status(a.status, MOE_ERR_BAD_ROW);  // skipped
         else
-          n[i] = static_cast<int>((cnt + kTileT - 1) / kTileT);
+          n[i] = static_cast<int>((cnt + S::kTileT - 1) / S::kTileT);
       }
       sum += n[i];
     }
@@ -232,41 +321,54 @@ grouped_mx4_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
     int before = incl - sum;
     for (int w = 0; w < warp; ++w) before += s.warp_sums[w];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int e = tid * 4 + i;
-      if (e <= a.E) s.first_tile[e] = before;
+    for (int i = 0; i < kPer; ++i) {
+      const int e = tid * kPer + i;
+      if (e <= a.E) s.first_tile[e] = before;  // (a.E <= 1024: thread 256 writes the last)
       before += n[i];
     }
-    if (tid == kThreads - 1 && a.E == kMaxExperts) s.first_tile[kMaxExperts] = before;
   }
   tmem_fence_before();
   __syncthreads();
+  if constexpr (CG == 2) {  // the other CTA's barriers are initialised
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
   tmem_fence_after();
   const uint32_t tmem = s.tmem;
   volatile int* abort = &s.abort;
 
   if (warp == 0) {
     if (lane == 0) {
-      Tiles tl(a, s.first_tile);
+      Tiles<CG> tl(a, s.first_tile);
       int st = 0;
       uint32_t round = 0;
       int64_t issued = 0;
       bool ok = true;
       while (ok && tl.next()) {
-        const int boxes = (tl.cols() + kBoxT - 1) / kBoxT;
-        const int64_t wr = static_cast<int64_t>(tl.e) * a.N + static_cast<int64_t>(tl.f) * (a.gate ? kBoxF : kTileF);
-        const int w0 = static_cast<int>(wr), w1 = w0 + (a.gate ? a.N / 2 : kBoxF);
+        const int half = tl.cols() / CG;  // columns whose rows this CTA loads
+        const int boxes = half / kBoxRows;
+        const int wr = static_cast<int>(tl.weight_row0()), up = a.N / 2;
+        const int xr = tl.row0 + rank * half;
         for (int kb = 0; kb < a.kstages; ++kb) {
           if (!wait_stage(&s.empty[st], (round & 1u) ^ 1u, abort, a.status)) {
             ok = false;
             break;
           }
-          moe::mbar_arrive_expect_tx(&s.full[st], kBytesA + boxes * (kBoxT * 128));
+          moe::mbar_arrive_expect_tx(&s.full[st], kBytesA + boxes * (kBoxRows * 128));
           const int x = kb * 128;
-          tma_load_2d(s.ab[st], &map_w, x, w0, &s.full[st]);
-          tma_load_2d(s.ab[st] + kBytesA / 2, &map_w, x, w1, &s.full[st]);
+          uint8_t* dst = s.ab[st];
+          if (a.gate) {
+#pragma unroll
+            for (int b = 0; b < kTileF / (2 * kBoxRows); ++b) {
+              tma_load_2d(dst + (2 * b) * kBoxRows * 128, &map_w, x, wr + b * kBoxRows, &s.full[st]);
+              tma_load_2d(dst + (2 * b + 1) * kBoxRows * 128, &map_w, x, wr + up + b * kBoxRows, &s.full[st]);
+            }
+          } else {
+            tma_load_2d(dst, &map_w, x, wr, &s.full[st]);
+          }
+          dst += kBytesA;
           for (int b = 0; b < boxes; ++b)
-            tma_load_2d(s.ab[st] + kBytesA + b * (kBoxT * 128), &map_x, x, tl.row0 + b * kBoxT, &s.full[st]);
+            tma_load_2d(dst + b * (kBoxRows * 128), &map_x, x, xr + b * kBoxRows, &s.full[st]);
           ++issued;
           if (++st == kStages) { st = 0; ++round; }
         }
@@ -277,78 +379,102 @@ grouped_mx4_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      // instruction descriptor: A and B e2m1, scales e8m0, 128 lanes; columns and scale ids below
-      constexpr uint32_t kDesc = (1u << 7) | (1u << 10) | (1u << 23) | ((128u >> 4) << 24);
-      Tiles tl(a, s.first_tile);
+    if (lane == 0 && rank == 0) {
+      // instruction descriptor: A and B e2m1, scales e8m0, 128 lanes a CTA; columns and scale ids below
+      constexpr uint32_t kDesc = (1u << 7) | (1u << 10) | (1u << 23) | ((CG * 128u >> 4) << 24);
+      Tiles<CG> tl(a, s.first_tile);
       int st = 0;
-      uint32_t round = 0, buf = 0, buf_round = 0;
+      uint32_t round = 0, buf = 0, buf_round = 0, set = 0;
+      int64_t stage = 0;  // stages since the start
       bool ok = true;
       while (ok && tl.next()) {
-        if (!wait_stage(&s.acc_empty[buf], (buf_round & 1u) ^ 1u, abort, a.status)) break;
+        if (!wait_stage<CG == 2>(&s.acc_empty[buf], (buf_round & 1u) ^ 1u, abort, a.status)) break;
         tmem_fence_after();
         const uint32_t cols = static_cast<uint32_t>(tl.cols());
         const uint32_t idesc = kDesc | ((cols >> 3) << 17);
-        const uint32_t d = tmem + buf * kTileT;
-        for (int kb = 0; kb < a.kstages; ++kb) {
-          if (!wait_stage(&s.full[st], round & 1u, abort, a.status)) {
+        const uint32_t d = tmem + buf * S::kTileT;
+        for (int kb = 0; kb < a.kstages; ++kb, ++stage) {
+          bool here = wait_stage(&s.full[st], round & 1u, abort, a.status);
+          if (CG == 2) here = here && wait_stage<true>(&s.peer_full[st], round & 1u, abort, a.status);
+          // the products that read this set of TMEM scales, two stages ago, are done
+          if (stage >= 2) {
+            const int64_t q = stage - 2;
+            here = here && wait_stage(&s.empty[q % kStages], static_cast<uint32_t>(q / kStages) & 1u, abort, a.status);
+          }
+          if (!here) {
             ok = false;
             break;
           }
           tmem_fence_after();
-          const uint32_t sf = tmem + kTmemSf + static_cast<uint32_t>(st) * kTmemSfStage;
+          const uint32_t sf = tmem + S::kTmemSf + set * S::kSfCols;
           const uint32_t sf_smem = moe::smem_addr(s.sf[st]);
 #pragma unroll
-          for (int i = 0; i < kBytesSf / kAtom; ++i) sf_to_tmem(sf + 4 * i, sf_smem + i * kAtom);
+          for (int i = 0; i < S::kBytesSf / kAtom; ++i) sf_to_tmem<CG>(sf + 4 * i, sf_smem + i * kAtom);
           const uint64_t da = desc_sw128(moe::smem_addr(s.ab[st]));
           const uint64_t db = desc_sw128(moe::smem_addr(s.ab[st] + kBytesA));
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {  // 64 elements: 32 bytes further in the swizzle atom
             const uint32_t id = (kk & 1) * 2;  // which two of the chunk's four scales
-            mma_mx4(d, da + kk * 2, db + kk * 2, idesc | (id << 4) | (id << 29), sf + 4 * (kk >> 1),
-                    sf + 8 + 4 * (kTileT / 128) * (kk >> 1), kb > 0 || kk > 0);
+            mma_mx4<CG>(d, da + kk * 2, db + kk * 2, idesc | (id << 4) | (id << 29), sf + 4 * (kk >> 1),
+                        sf + 8 + 4 * S::kAtomsB * (kk >> 1), kb > 0 || kk > 0);
           }
-          commit(&s.empty[st]);
+          commit<CG>(&s.empty[st]);
+          set ^= 1u;
           if (++st == kStages) { st = 0; ++round; }
         }
         if (!ok) break;
-        commit(&s.acc_full[buf]);
+        commit<CG>(&s.acc_full[buf]);
         if (++buf == 2) { buf = 0; ++buf_round; }
       }
       if (*abort != 0) {  // products in flight still read shared memory and write TMEM
-        commit(&s.drained);
+        commit<CG>(&s.drained);
         moe::mbar_wait(&s.drained, 0, 200000000ull);
+      }
+    } else if (lane == 0) {  // the pair's second CTA: tell the first that a stage is there
+      Tiles<CG> tl(a, s.first_tile);
+      int st = 0;
+      uint32_t round = 0;
+      bool ok = true;
+      while (ok && tl.next()) {
+        for (int kb = 0; kb < a.kstages; ++kb) {
+          if (!wait_stage(&s.full[st], round & 1u, abort, a.status)) {
+            ok = false;
+            break;
+          }
+          arrive_first(&s.peer_full[st]);
+          if (++st == kStages) { st = 0; ++round; }
+        }
       }
     }
   } else if (warp < 4) {
     // scales: chunk 2 kb + (warp - 2) of each stage, for lane l the words of rows l, 32 + l, 64 + l, 96 + l
-    Tiles tl(a, s.first_tile);
+    Tiles<CG> tl(a, s.first_tile);
+    // (nothing is computed from a word before its stage's turn: the loads stay in flight)
+    constexpr uint32_t kOne = 0x7f7f7f7fu;
     const int which = warp - 2;
-    int kb = 0;
+    int kb = 0, kb_st = 0;
+    // bytes of blocks past K in the last chunk: 1, whatever is there (the codes are zeros, but NaN times zero is NaN)
+    const int past = a.chunks * 4 - a.K / 32;
+    const uint32_t keep_last = past > 0 ? 0xffffffffu >> (8 * past) : 0xffffffffu;
     bool more = tl.next();
-    uint4 va[kSfAhead], vb[kSfAhead][kTileT / 128];
+    uint4 va[kSfAhead], vb[kSfAhead][S::kAtomsB];
     bool have[kSfAhead];
     const int64_t w_rows = static_cast<int64_t>(a.E) * a.N;
     auto load = [&](int i) {
       have[i] = more;
       if (!more) return;
       const int c = kb * 2 + which;
-      constexpr uint32_t kOne = 0x7f7f7f7fu;
       va[i] = make_uint4(kOne, kOne, kOne, kOne);
 #pragma unroll
-      for (int h = 0; h < kTileT / 128; ++h) vb[i][h] = va[i];
+      for (int h = 0; h < S::kAtomsB; ++h) vb[i][h] = va[i];
       if (c < a.chunks) {
-        // bytes of blocks past K: 1, whatever is there (the codes are zeros, but NaN times zero is NaN)
-        const int past = (c + 1) * 4 - a.K / 32;
-        const uint32_t keep = past > 0 ? 0xffffffffu >> (8 * past) : 0xffffffffu;
-        auto ours = [&](uint32_t v) -> uint32_t { return (v & keep) | (kOne & ~keep); };
         const uint32_t* w = a.w_sf + c * w_rows;
-        va[i] = make_uint4(ours(__ldg(w + tl.weight_row(lane))), ours(__ldg(w + tl.weight_row(lane + 32))),
-                           ours(__ldg(w + tl.weight_row(lane + 64))), ours(__ldg(w + tl.weight_row(lane + 96))));
+        va[i] = make_uint4(__ldg(w + tl.weight_row(lane)), __ldg(w + tl.weight_row(lane + 32)),
+                           __ldg(w + tl.weight_row(lane + 64)), __ldg(w + tl.weight_row(lane + 96)));
         const uint32_t* x = a.x_sf + c * a.capacity;
-        auto word = [&](int n) -> uint32_t { return n < tl.rows ? ours(__ldg(x + tl.row0 + n)) : kOne; };
+        auto word = [&](int n) -> uint32_t { return n < tl.rows ? __ldg(x + tl.row0 + n) : kOne; };
 #pragma unroll
-        for (int h = 0; h < kTileT / 128; ++h)
+        for (int h = 0; h < S::kAtomsB; ++h)
           vb[i][h] = make_uint4(word(h * 128 + lane), word(h * 128 + 32 + lane), word(h * 128 + 64 + lane),
                                 word(h * 128 + 96 + lane));
       }
@@ -373,11 +499,17 @@ grouped_mx4_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
           ok = false;
           continue;
         }
+        const uint32_t keep = kb_st * 2 + which == a.chunks - 1 ? keep_last : 0xffffffffu;
+        if (++kb_st == a.kstages) kb_st = 0;
+        auto put = [&](uint8_t* dst, const uint4& v) {
+          const uint32_t one = kOne & ~keep;
+          *reinterpret_cast<uint4*>(dst + lane * 16) =
+              make_uint4((v.x & keep) | one, (v.y & keep) | one, (v.z & keep) | one, (v.w & keep) | one);
+        };
         uint8_t* sf = s.sf[st];
-        *reinterpret_cast<uint4*>(sf + which * kAtom + lane * 16) = va[i];
+        put(sf + which * kAtom, va[i]);
 #pragma unroll
-        for (int h = 0; h < kTileT / 128; ++h)
-          *reinterpret_cast<uint4*>(sf + 2 * kAtom + (which * (kTileT / 128) + h) * kAtom + lane * 16) = vb[i][h];
+        for (int h = 0; h < S::kAtomsB; ++h) put(sf + 2 * kAtom + (which * S::kAtomsB + h) * kAtom, vb[i][h]);
         moe::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) moe::mbar_arrive(&s.full[st]);
@@ -386,68 +518,90 @@ grouped_mx4_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
       }
     }
   } else {
-    Tiles tl(a, s.first_tile);
-    const int et = tid - 128, quad = warp - 4;
+    Tiles<CG> tl(a, s.first_tile);
+    const int quad = warp & 3, turn = (warp - 4) >> 2;  // lanes 32 quad .. +31, column blocks turn, turn + 2, ...
+    __nv_bfloat16* epi = s.epi[warp - 4];
+    const uint32_t epi_addr = moe::smem_addr(epi);
     uint32_t buf = 0, buf_round = 0;
     while (tl.next()) {
-      // one thread waits, so that the four warps agree whether the accumulator came
-      if (et == 0) s.epi_go = wait_stage(&s.acc_full[buf], buf_round & 1u, abort, a.status) ? 1 : 0;
-      moe::named_barrier(1, 128);
-      if (s.epi_go == 0) break;
-      while (!moe::mbar_try_wait(&s.acc_full[buf], buf_round & 1u)) {
-      }  // completed already: each thread's own acquire
+      if (!__all_sync(0xffffffffu, wait_stage(&s.acc_full[buf], buf_round & 1u, abort, a.status))) break;
       tmem_fence_after();
       const int cols = tl.cols();
-      for (int c0 = 0; c0 < cols; c0 += kEpiT) {
-        uint32_t v[32];
-        tmem_ld32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * kTileT + c0, v);
-        if (c0 + kEpiT >= cols) {
-          tmem_fence_before();
-          __syncwarp();
-          if (lane == 0) moe::mbar_arrive(&s.acc_empty[buf]);
-        }
-        moe::named_barrier(1, 128);  // the previous rows have been read
-#pragma unroll
-        for (int j = 0; j < 32; ++j) s.epi[j * kEpiStride + quad * 32 + lane] = __uint_as_float(v[j]);
-        moe::named_barrier(1, 128);
+      const int64_t col0 = a.gate ? static_cast<int64_t>(tl.f) * (kTileF / 2) + quad * 16
+                                  : static_cast<int64_t>(tl.f) * kTileF + quad * 32;
+      for (int c0 = turn * kEpiT; c0 < cols; c0 += 2 * kEpiT) {
+        uint32_t lo[16], hi[16];  // lanes 0..15 and 16..31: with the gate, gate and up
+        const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * S::kTileT + c0;
+        tmem_ld16x32(taddr, lo);
+        tmem_ld16x32(taddr + (16u << 16), hi);
+        tmem_wait_ld();
+        __syncwarp();  // the previous block has been read
         const int left = tl.rows - c0 < kEpiT ? tl.rows - c0 : kEpiT;
-        __nv_bfloat16* out = a.out + static_cast<int64_t>(tl.row0 + c0) * a.ld_out;
-        if (a.gate) {
-          for (int i = et; i < left * 8; i += 128) {
-            const int j = i >> 3, g = (i & 7) * 8;
-            const int64_t col = static_cast<int64_t>(tl.f) * kBoxF + g;
-            if (col >= a.ld_out) continue;
-            const float* p = s.epi + j * kEpiStride + g;
-            uint32_t o[4];
+        __nv_bfloat16* out = a.out + static_cast<int64_t>(tl.row0 + c0) * a.ld_out + col0;
+        if (a.gate) {  // 16 features: 32 bytes a row
+#pragma unroll
+          for (int i = 0; i < 4; i += 2) {
+            uint32_t p[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              const float g0 = p[2 * q], g1 = p[2 * q + 1];
-              o[q] = moe::pack_bf16x2(__fdividef(g0, 1.f + __expf(-g0)) * p[kBoxF + 2 * q],
-                                      __fdividef(g1, 1.f + __expf(-g1)) * p[kBoxF + 2 * q + 1]);
+              const int v = 4 * i + 2 * q;
+              p[q] = moe::pack_bf16x2(silu_times(lo[v], hi[v]), silu_times(lo[v + 1], hi[v + 1]));
             }
-            moe::st_plain(reinterpret_cast<uint4*>(out + j * a.ld_out + col), make_uint4(o[0], o[1], o[2], o[3]));
+            // blocks: columns 8i, features 0..7 and 8..15; columns 8i + 8, the same
+            const int row = 8 * (i + (lane >> 4)) + (lane & 7);
+            stmatrix_trans(epi_addr + row * (kEpiStride * 2) + ((lane >> 3) & 1) * 16, p[0], p[1], p[2], p[3]);
           }
-        } else {
-          for (int i = et; i < left * 16; i += 128) {
-            const int j = i >> 4, g = (i & 15) * 8;
-            const int64_t col = static_cast<int64_t>(tl.f) * kTileF + g;
-            if (col >= a.ld_out) continue;
-            const float4 p = *reinterpret_cast<const float4*>(s.epi + j * kEpiStride + g);
-            const float4 q = *reinterpret_cast<const float4*>(s.epi + j * kEpiStride + g + 4);
-            moe::st_plain(reinterpret_cast<uint4*>(out + j * a.ld_out + col),
-                          make_uint4(moe::pack_bf16x2(p.x, p.y), moe::pack_bf16x2(p.z, p.w),
-                                     moe::pack_bf16x2(q.x, q.y), moe::pack_bf16x2(q.z, q.w)));
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int j = i * 16 + (lane >> 1), g = (lane & 1) * 8;
+            const uint4 v = moe::lds128(epi + j * kEpiStride + g);
+            if (j < left && col0 + g < a.ld_out)
+              moe::st_plain(reinterpret_cast<uint4*>(out + j * a.ld_out + g), v);
+          }
+        } else {  // 32 features: 64 bytes a row
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int v = 4 * i;
+            stmatrix_trans(epi_addr + (8 * i + (lane & 7)) * (kEpiStride * 2) + (lane >> 3) * 16,
+                           moe::pack_bf16x2(__uint_as_float(lo[v]), __uint_as_float(lo[v + 1])),
+                           moe::pack_bf16x2(__uint_as_float(lo[v + 2]), __uint_as_float(lo[v + 3])),
+                           moe::pack_bf16x2(__uint_as_float(hi[v]), __uint_as_float(hi[v + 1])),
+                           moe::pack_bf16x2(__uint_as_float(hi[v + 2]), __uint_as_float(hi[v + 3])));
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int j = i * 8 + (lane >> 2), g = (lane & 3) * 8;
+            const uint4 v = moe::lds128(epi + j * kEpiStride + g);
+            if (j < left && col0 + g < a.ld_out)
+              moe::st_plain(reinterpret_cast<uint4*>(out + j * a.ld_out + g), v);
           }
         }
+      }
+      tmem_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (CG == 1 || rank == 0)
+          moe::mbar_arrive(&s.acc_empty[buf]);
+        else
+          arrive_first(&s.acc_empty[buf]);
       }
       if (++buf == 2) { buf = 0; ++buf_round; }
     }
   }
   tmem_fence_before();
   __syncthreads();
+  if constexpr (CG == 2) {  // the pair's products read both CTAs' memory, and its barriers are reached from both
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
   if (warp == 1) {
     tmem_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+    if constexpr (CG == 1)
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+    else
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
   }
 }
 
@@ -478,6 +632,39 @@ bool codes_map(CUtensorMap* m, const void* codes, int64_t rows, int32_t K, uint3
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(codes), dims, strides, boxes, ones,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr int kPairRows = 64;  // rows an expert from which on pairs of CTAs take a tile
+
+template <int CG>
+moe_status_t launch_product(ProductArgs a, const CUtensorMap& mx, const CUtensorMap& mw, cudaStream_t st) {
+  const int per = CG * (a.gate ? kTileF / 2 : kTileF);
+  a.ftiles = static_cast<int>((a.ld_out + per - 1) / per);
+  const int sms = moe_host::sm_count();
+  if (sms <= 0) return MOE_ERR_CUDA;
+  // no more CTAs than tiles there can be: a row tile per expert and per kTileT rows
+  const int64_t most = ((a.E < a.capacity ? a.E : a.capacity) + a.capacity / Shape<CG>::kTileT) * a.ftiles;
+  const int64_t grid = (most < sms / CG ? most : sms / CG) * CG;
+  const size_t smem = sizeof(typename Shape<CG>::Smem) + 1024;
+  const void* kernel = reinterpret_cast<const void*>(&grouped_mx4_kernel<CG>);
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) !=
+          cudaSuccess ||
+      moe_host::prefer_max_shared(kernel) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CG;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = CG == 1 ? 1 : 2;
+  return cudaLaunchKernelEx(&cfg, grouped_mx4_kernel<CG>, mx, mw, a) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // namespace
@@ -511,24 +698,14 @@ extern "C" moe_status_t moe_grouped_gemm_mx4(const void* x_codes, const void* x_
   a.kstages = (K + kStageK - 1) / kStageK;
   a.gate = gate ? 1 : 0;
   a.ld_out = gate ? N / 2 : N;
-  const int per = gate ? kBoxF : kTileF;
-  a.ftiles = static_cast<int>((a.ld_out + per - 1) / per);
   a.capacity = capacity;
   a.out = static_cast<__nv_bfloat16*>(out);
   a.status = device_status;
   CUtensorMap mx, mw;
-  if (!codes_map(&mx, x_codes, capacity, K, kBoxT) ||
-      !codes_map(&mw, w_codes, static_cast<int64_t>(E_local) * N, K, kBoxF))
+  if (!codes_map(&mx, x_codes, capacity, K, kBoxRows) ||
+      !codes_map(&mw, w_codes, static_cast<int64_t>(E_local) * N, K, gate ? kBoxRows : kTileF))
     return MOE_ERR_CUDA;
-  const int sms = moe_host::sm_count();
-  if (sms <= 0) return MOE_ERR_CUDA;
-  // no more CTAs than tiles there can be: a row tile per expert and per kTileT rows
-  const int64_t most = (E_local < capacity ? E_local : capacity) + capacity / kTileT;
-  const int64_t grid = most * a.ftiles < sms ? most * a.ftiles : sms;
-  const size_t smem = sizeof(Smem) + 1024;
-  if (cudaFuncSetAttribute(grouped_mx4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) !=
-      cudaSuccess)
-    return MOE_ERR_CUDA;
-  return moe_host::launch_pdl_max_shared(grouped_mx4_kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), smem,
-                                         static_cast<cudaStream_t>(stream), mx, mw, a);
+  // many rows an expert: pairs of CTAs
+  return capacity >= int64_t{E_local} * kPairRows ? launch_product<2>(a, mx, mw, static_cast<cudaStream_t>(stream))
+                                                  : launch_product<1>(a, mx, mw, static_cast<cudaStream_t>(stream));
 }
