@@ -33,7 +33,7 @@ constexpr int kThreads = 384;
 constexpr int kEpiWarps = 8;
 constexpr int kTileF = 128;             // features a CTA and tile
 constexpr int kStageK = 256;            // elements of K a stage: 128 bytes, one swizzle atom
-constexpr int kBoxRows = 16;            // rows of x a TMA box; of the weights with the gate (16 gate, 16 up, ...)
+constexpr int kBoxRows = 16;            // rows of x in TMA boxes of 16, 32 and 64; gate features before the up ones
 constexpr int kBytesA = kTileF * kStageK / 2;
 constexpr int kAtom = 512;              // scales of 128 rows by 128 elements
 constexpr int kEpiT = 32;               // columns an epilogue warp takes at a time
@@ -56,7 +56,7 @@ struct Shape {
   static constexpr uint32_t kSfCols = 8 + 8 * kAtomsB;
   static constexpr uint32_t kTmemSf = 2 * kTileT;
   static_assert(kTmemSf + 2 * kSfCols <= kTmemCols, "TMEM columns");
-  static_assert(kStageBytes % 1024 == 0 && kRowsB % kBoxRows == 0, "swizzle atoms");
+  static_assert(kStageBytes % 1024 == 0 && kRowsB % kBoxRows == 0 && kRowsB < 128, "swizzle atoms, boxes");
 
   struct __align__(1024) Smem {
     uint8_t ab[kStages][kStageBytes];  // A then B, 128-byte swizzled
@@ -64,7 +64,7 @@ struct Shape {
     __nv_bfloat16 epi[kEpiWarps][kEpiT * kEpiStride];
     int32_t first_tile[kMaxExperts + 1];  // row tiles before expert e
     int32_t warp_sums[kThreads / 32];
-    uint64_t full[kStages], peer_full[kStages], empty[kStages], acc_full[2], acc_empty[2], drained;
+    uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drained;
     uint32_t tmem;
     int abort;
   };
@@ -81,11 +81,20 @@ struct ProductArgs {
   int kstages;    // ceil(K / 256)
   int ftiles;     // feature tiles (of a CTA, or of a pair)
   int gate;       // 1: silu(gate) * up
+  int gate_box;   // 1: map_w has the gate's boxes (N a multiple of 32), 0: boxes of 16 rows
   int64_t capacity;
   __nv_bfloat16* out;
   int64_t ld_out;  // N or N / 2
   int32_t* status;
 };
+
+// x, 0, 0, group, expert: with the gate, four groups of 16 gate and the 16 matching up features
+__device__ __forceinline__ void tma_load_gate(void* dst, const CUtensorMap* map, int x, int group, int e, uint64_t* bar) {
+  asm volatile("cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %3, %4, %5}], [%6];" ::"r"(
+                   moe::smem_addr(dst)),
+               "l"(map), "r"(x), "r"(0), "r"(group), "r"(e), "r"(moe::smem_addr(bar))
+               : "memory");
+}
 
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
   asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
@@ -106,11 +115,11 @@ __device__ __forceinline__ uint64_t desc_plain(uint32_t addr) {
 
 // 512 bytes of scales to four TMEM columns; in a pair, each CTA's own shared memory to its own TMEM.
 template <int CG>
-__device__ __forceinline__ void sf_to_tmem(uint32_t taddr, uint32_t smem) {
+__device__ __forceinline__ void sf_to_tmem(uint32_t taddr, uint64_t smem_desc) {
   if constexpr (CG == 1)
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc_plain(smem)) : "memory");
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(smem_desc) : "memory");
   else
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc_plain(smem)) : "memory");
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(smem_desc) : "memory");
 }
 
 template <int CG>
@@ -153,15 +162,26 @@ __device__ __forceinline__ void arrive_first(uint64_t* bar) {
       : "memory");
 }
 
-__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
+// Non-blocking test of a phase (kCluster: with the other CTA's writes before its arrival).
+template <bool kCluster>
+__device__ __forceinline__ bool phase_done(uint64_t* bar, uint32_t parity) {
   uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(moe::smem_addr(bar)), "r"(parity)
-      : "memory");
+  if constexpr (kCluster)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(moe::smem_addr(bar)), "r"(parity)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(moe::smem_addr(bar)), "r"(parity)
+        : "memory");
   return done != 0u;
 }
 __device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -191,50 +211,80 @@ __device__ __forceinline__ float silu_times(uint32_t gate, uint32_t up) {
   return __fdividef(g, 1.f + __expf(-g)) * __uint_as_float(up);
 }
 
-// A bounded wait that polls without sleeping (the wait itself suspends in hardware); it also gives up when another
-// role of the CTA has.
-template <bool kCluster = false>
-__device__ __forceinline__ bool wait_stage(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* status) {
-  auto poll = [&] { return kCluster ? try_wait_cluster(bar, parity) : moe::mbar_try_wait(bar, parity); };
-  if (poll()) return true;
-  const uint64_t t0 = moe::global_ns();
+// A bounded wait of a warp; it also gives up when another role of the CTA has.  The first test is inline and its vote
+// uniform, so that the loops around it stay convergent: the issuing warps must not run as a lone lane, whose operands
+// go one by one through vector registers (1675 cycles to issue a stage that takes 450 to compute).
+template <bool kCluster>
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* status) {
+  uint64_t t0 = 0;
   for (;;) {
 #pragma unroll 1
-    for (int i = 0; i < 64; ++i)
-      if (poll()) return true;
+    for (int i = 0; i < 256; ++i)
+      if (phase_done<kCluster>(bar, parity)) return true;
     if (*abort != 0) return false;
-    if (moe::global_ns() - t0 > moe::kWaitLimitNs) {
+    const uint64_t t = moe::global_ns();
+    if (t0 == 0) t0 = t;
+    if (t - t0 > moe::kWaitLimitNs) {
       moe::record_status(status, MOE_ERR_TIMEOUT);
       *abort = 1;
       return false;
     }
   }
 }
+template <bool kCluster = false>
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* status) {
+  if (__all_sync(0xffffffffu, phase_done<kCluster>(bar, parity))) return true;
+  return __all_sync(0xffffffffu, wait_slow<kCluster>(bar, parity, abort, status));
+}
 
-// The tiles of this CTA (or pair), in order: expert by expert, then row tiles, features fastest.
+// One lane of a converged warp, always the same.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0u;
+}
+
+// The tiles of this CTA (or pair), in order: expert by expert, then row tiles, features fastest.  The next tile's
+// count and offset are read one tile ahead (a first use costs an L2 round trip).
 template <int CG>
 struct Tiles {
   const ProductArgs& a;
   const int32_t* first;  // row tiles before expert e
-  int64_t t, end;
   int e = 0;
   int f, row0, rows;  // this CTA's feature tile, the tile's first row, its rows
+  int rt, ft, step_rt, step_ft;     // the next tile: row tile, feature tile; and the stride between this CTA's tiles
+  int next_e = 0, next_cnt, next_off;
 
-  __device__ Tiles(const ProductArgs& args, const int32_t* first_tile)
-      : a(args), first(first_tile), t(static_cast<int64_t>(blockIdx.x / CG) - gridDim.x / CG),
-        end(static_cast<int64_t>(first_tile[args.E]) * args.ftiles) {}
+  __device__ Tiles(const ProductArgs& args, const int32_t* first_tile) : a(args), first(first_tile) {
+    const int at = blockIdx.x / CG, stride = gridDim.x / CG;
+    rt = at / a.ftiles;
+    ft = at - rt * a.ftiles;
+    step_rt = stride / a.ftiles;
+    step_ft = stride - step_rt * a.ftiles;
+    ahead();
+  }
+  __device__ void ahead() {
+    if (rt >= first[a.E]) return;
+    while (first[next_e + 1] <= rt) ++next_e;
+    next_cnt = a.counts[next_e];
+    next_off = a.offsets[next_e];
+  }
   __device__ bool next() {
-    t += gridDim.x / CG;
-    if (t >= end) return false;
-    const int rt = static_cast<int>(t / a.ftiles);
-    f = static_cast<int>(t - static_cast<int64_t>(rt) * a.ftiles) * CG + (CG == 1 ? 0 : blockIdx.x % CG);
-    while (first[e + 1] <= rt) ++e;
-    const int cnt = a.counts[e], n = first[e + 1] - first[e];
+    if (rt >= first[a.E]) return false;
+    e = next_e;
+    f = ft * CG + (CG == 1 ? 0 : blockIdx.x % CG);
+    const int n = first[e + 1] - first[e], i = rt - first[e];
     constexpr int kStep = Shape<CG>::kStepT;
-    const int per = ((cnt + n - 1) / n + kStep - 1) / kStep * kStep;  // at most kTileT
-    const int i = rt - first[e];
-    row0 = a.offsets[e] + i * per;
-    rows = cnt - i * per < per ? cnt - i * per : per;
+    const int per = ((next_cnt + n - 1) / n + kStep - 1) / kStep * kStep;  // at most kTileT
+    row0 = next_off + i * per;
+    rows = next_cnt - i * per < per ? next_cnt - i * per : per;
+    rt += step_rt;
+    ft += step_ft;
+    if (ft >= a.ftiles) {
+      ft -= a.ftiles;
+      ++rt;
+    }
+    ahead();
     return true;
   }
   // the product's columns
@@ -253,7 +303,8 @@ struct Tiles {
 
 template <int CG>
 __global__ void __launch_bounds__(kThreads, 1)
-grouped_mx4_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
+grouped_mx4_kernel(const __grid_constant__ CUtensorMap map_x16, const __grid_constant__ CUtensorMap map_x32,
+                   const __grid_constant__ CUtensorMap map_x64, const __grid_constant__ CUtensorMap map_w,
                    const ProductArgs a) {
   using S = Shape<CG>;
   constexpr int kStages = S::kStages;
@@ -264,8 +315,8 @@ grouped_mx4_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
   const int rank = CG == 1 ? 0 : blockIdx.x % CG;  // in the pair
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
-      moe::mbar_init(&s.full[i], 3);  // the TMA warp and the two scale warps
-      moe::mbar_init(&s.peer_full[i], 1);
+      // the TMA warp and the two scale warps; in a pair, at the first CTA, the second's stage too
+      moe::mbar_init(&s.full[i], CG == 2 && rank == 0 ? 4 : 3);
       moe::mbar_init(&s.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -338,80 +389,91 @@ grouped_mx4_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
   volatile int* abort = &s.abort;
 
   if (warp == 0) {
-    if (lane == 0) {
-      Tiles<CG> tl(a, s.first_tile);
-      int st = 0;
-      uint32_t round = 0;
-      int64_t issued = 0;
-      bool ok = true;
-      while (ok && tl.next()) {
-        const int half = tl.cols() / CG;  // columns whose rows this CTA loads
-        const int boxes = half / kBoxRows;
-        const int wr = static_cast<int>(tl.weight_row0()), up = a.N / 2;
-        const int xr = tl.row0 + rank * half;
-        for (int kb = 0; kb < a.kstages; ++kb) {
-          if (!wait_stage(&s.empty[st], (round & 1u) ^ 1u, abort, a.status)) {
-            ok = false;
-            break;
-          }
-          moe::mbar_arrive_expect_tx(&s.full[st], kBytesA + boxes * (kBoxRows * 128));
+    Tiles<CG> tl(a, s.first_tile);
+    int st = 0;
+    uint32_t round = 0;
+    int64_t issued = 0;
+    bool ok = true;
+    while (ok && tl.next()) {
+      const int half = tl.cols() / CG;  // columns whose rows this CTA loads
+      const int wr = static_cast<int>(tl.weight_row0()), up = a.N / 2;
+      const int xr = tl.row0 + rank * half;
+      for (int kb = 0; kb < a.kstages; ++kb) {
+        if (!wait_warp(&s.empty[st], (round & 1u) ^ 1u, abort, a.status)) {
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
+          moe::mbar_arrive_expect_tx(&s.full[st], kBytesA + half * 128);
           const int x = kb * 128;
           uint8_t* dst = s.ab[st];
-          if (a.gate) {
+          if (!a.gate) {
+            tma_load_2d(dst, &map_w, x, wr, &s.full[st]);
+          } else if (a.gate_box) {
+            tma_load_gate(dst, &map_w, x, tl.f * (kTileF / 2 / kBoxRows), tl.e, &s.full[st]);
+          } else {
 #pragma unroll
             for (int b = 0; b < kTileF / (2 * kBoxRows); ++b) {
               tma_load_2d(dst + (2 * b) * kBoxRows * 128, &map_w, x, wr + b * kBoxRows, &s.full[st]);
               tma_load_2d(dst + (2 * b + 1) * kBoxRows * 128, &map_w, x, wr + up + b * kBoxRows, &s.full[st]);
             }
-          } else {
-            tma_load_2d(dst, &map_w, x, wr, &s.full[st]);
           }
-          dst += kBytesA;
-          for (int b = 0; b < boxes; ++b)
-            tma_load_2d(dst + b * (kBoxRows * 128), &map_x, x, xr + b * kBoxRows, &s.full[st]);
-          ++issued;
-          if (++st == kStages) { st = 0; ++round; }
+          dst += kBytesA;  // then the rows, in the fewest boxes: each costs the copy engine about 70 cycles
+          int done = 0;
+          if (half & 64) {
+            tma_load_2d(dst, &map_x64, x, xr, &s.full[st]);
+            done = 64;
+          }
+          if (half & 32) {
+            tma_load_2d(dst + done * 128, &map_x32, x, xr + done, &s.full[st]);
+            done += 32;
+          }
+          if (half & 16) tma_load_2d(dst + done * 128, &map_x16, x, xr + done, &s.full[st]);
         }
-      }
-      if (*abort != 0) {  // never leave with loads in flight into this CTA's shared memory
-        for (int64_t q = issued > kStages ? issued - kStages : 0; q < issued; ++q)
-          moe::mbar_wait(&s.full[q % kStages], static_cast<uint32_t>(q / kStages) & 1u, 200000000ull);
+        __syncwarp();
+        ++issued;
+        if (++st == kStages) { st = 0; ++round; }
       }
     }
-  } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
-      // instruction descriptor: A and B e2m1, scales e8m0, 128 lanes a CTA; columns and scale ids below
-      constexpr uint32_t kDesc = (1u << 7) | (1u << 10) | (1u << 23) | ((CG * 128u >> 4) << 24);
-      Tiles<CG> tl(a, s.first_tile);
-      int st = 0;
-      uint32_t round = 0, buf = 0, buf_round = 0, set = 0;
-      int64_t stage = 0;  // stages since the start
-      bool ok = true;
-      while (ok && tl.next()) {
-        if (!wait_stage<CG == 2>(&s.acc_empty[buf], (buf_round & 1u) ^ 1u, abort, a.status)) break;
+    if (*abort != 0) {  // never leave with loads in flight into this CTA's shared memory
+      for (int64_t q = issued > kStages ? issued - kStages : 0; q < issued; ++q)
+        moe::mbar_wait(&s.full[q % kStages], static_cast<uint32_t>(q / kStages) & 1u, 200000000ull);
+    }
+  } else if (warp == 1 && rank == 0) {
+    // instruction descriptor: A and B e2m1, scales e8m0, 128 lanes a CTA; columns and scale ids below
+    constexpr uint32_t kDesc = (1u << 7) | (1u << 10) | (1u << 23) | ((CG * 128u >> 4) << 24);
+    Tiles<CG> tl(a, s.first_tile);
+    const uint64_t da0 = desc_sw128(moe::smem_addr(s.ab[0])), sf0 = desc_plain(moe::smem_addr(s.sf[0]));
+    int st = 0;
+    uint32_t round = 0, buf = 0, buf_round = 0, set = 0;
+    int st2 = 0;  // the stage two before this one, and its round
+    uint32_t round2 = 0;
+    bool first = true, second = false, ok = true;
+    while (ok && tl.next()) {
+      if (!wait_warp<CG == 2>(&s.acc_empty[buf], (buf_round & 1u) ^ 1u, abort, a.status)) break;
+      tmem_fence_after();
+      const uint32_t idesc = kDesc | ((static_cast<uint32_t>(tl.cols()) >> 3) << 17);
+      const uint32_t d = tmem + buf * S::kTileT;
+      for (int kb = 0; kb < a.kstages; ++kb) {
+        bool here = wait_warp<CG == 2>(&s.full[st], round & 1u, abort, a.status);
+        // the products that read this set of TMEM scales, two stages ago, are done
+        if (!first && !second) {
+          here = here && wait_warp(&s.empty[st2], round2 & 1u, abort, a.status);
+          if (++st2 == kStages) { st2 = 0; ++round2; }
+        }
+        second = first;
+        first = false;
+        if (!here) {
+          ok = false;
+          break;
+        }
         tmem_fence_after();
-        const uint32_t cols = static_cast<uint32_t>(tl.cols());
-        const uint32_t idesc = kDesc | ((cols >> 3) << 17);
-        const uint32_t d = tmem + buf * S::kTileT;
-        for (int kb = 0; kb < a.kstages; ++kb, ++stage) {
-          bool here = wait_stage(&s.full[st], round & 1u, abort, a.status);
-          if (CG == 2) here = here && wait_stage<true>(&s.peer_full[st], round & 1u, abort, a.status);
-          // the products that read this set of TMEM scales, two stages ago, are done
-          if (stage >= 2) {
-            const int64_t q = stage - 2;
-            here = here && wait_stage(&s.empty[q % kStages], static_cast<uint32_t>(q / kStages) & 1u, abort, a.status);
-          }
-          if (!here) {
-            ok = false;
-            break;
-          }
-          tmem_fence_after();
+        if (elect_one()) {
           const uint32_t sf = tmem + S::kTmemSf + set * S::kSfCols;
-          const uint32_t sf_smem = moe::smem_addr(s.sf[st]);
+          const uint64_t sfd = sf0 + static_cast<uint32_t>(st * (S::kBytesSf >> 4));
 #pragma unroll
-          for (int i = 0; i < S::kBytesSf / kAtom; ++i) sf_to_tmem<CG>(sf + 4 * i, sf_smem + i * kAtom);
-          const uint64_t da = desc_sw128(moe::smem_addr(s.ab[st]));
-          const uint64_t db = desc_sw128(moe::smem_addr(s.ab[st] + kBytesA));
+          for (int i = 0; i < S::kBytesSf / kAtom; ++i) sf_to_tmem<CG>(sf + 4 * i, sfd + i * (kAtom >> 4));
+          const uint64_t da = da0 + static_cast<uint32_t>(st * (S::kStageBytes >> 4)), db = da + (kBytesA >> 4);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {  // 64 elements: 32 bytes further in the swizzle atom
             const uint32_t id = (kk & 1) * 2;  // which two of the chunk's four scales
@@ -419,31 +481,33 @@ grouped_mx4_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
                         sf + 8 + 4 * S::kAtomsB * (kk >> 1), kb > 0 || kk > 0);
           }
           commit<CG>(&s.empty[st]);
-          set ^= 1u;
-          if (++st == kStages) { st = 0; ++round; }
+          if (kb == a.kstages - 1) commit<CG>(&s.acc_full[buf]);
         }
-        if (!ok) break;
-        commit<CG>(&s.acc_full[buf]);
-        if (++buf == 2) { buf = 0; ++buf_round; }
+        __syncwarp();
+        set ^= 1u;
+        if (++st == kStages) { st = 0; ++round; }
       }
-      if (*abort != 0) {  // products in flight still read shared memory and write TMEM
-        commit<CG>(&s.drained);
-        moe::mbar_wait(&s.drained, 0, 200000000ull);
-      }
-    } else if (lane == 0) {  // the pair's second CTA: tell the first that a stage is there
-      Tiles<CG> tl(a, s.first_tile);
-      int st = 0;
-      uint32_t round = 0;
-      bool ok = true;
-      while (ok && tl.next()) {
-        for (int kb = 0; kb < a.kstages; ++kb) {
-          if (!wait_stage(&s.full[st], round & 1u, abort, a.status)) {
-            ok = false;
-            break;
-          }
-          arrive_first(&s.peer_full[st]);
-          if (++st == kStages) { st = 0; ++round; }
+      if (++buf == 2) { buf = 0; ++buf_round; }
+    }
+    if (*abort != 0) {  // products in flight still read shared memory and write TMEM
+      if (elect_one()) commit<CG>(&s.drained);
+      __syncwarp();
+      moe::mbar_wait(&s.drained, 0, 200000000ull);
+    }
+  } else if (warp == 1) {  // the pair's second CTA: tell the first that a stage is there
+    Tiles<CG> tl(a, s.first_tile);
+    int st = 0;
+    uint32_t round = 0;
+    bool ok = true;
+    while (ok && tl.next()) {
+      for (int kb = 0; kb < a.kstages; ++kb) {
+        if (!wait_warp(&s.full[st], round & 1u, abort, a.status)) {
+          ok = false;
+          break;
         }
+        if (elect_one()) arrive_first(&s.full[st]);
+        __syncwarp();
+        if (++st == kStages) { st = 0; ++round; }
       }
     }
   } else if (warp < 4) {
@@ -495,7 +559,7 @@ grouped_mx4_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
           ok = false;
           continue;
         }
-        if (!__all_sync(0xffffffffu, wait_stage(&s.empty[st], (round & 1u) ^ 1u, abort, a.status))) {
+        if (!wait_warp(&s.empty[st], (round & 1u) ^ 1u, abort, a.status)) {
           ok = false;
           continue;
         }
@@ -524,7 +588,7 @@ grouped_mx4_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
     const uint32_t epi_addr = moe::smem_addr(epi);
     uint32_t buf = 0, buf_round = 0;
     while (tl.next()) {
-      if (!__all_sync(0xffffffffu, wait_stage(&s.acc_full[buf], buf_round & 1u, abort, a.status))) break;
+      if (!wait_warp(&s.acc_full[buf], buf_round & 1u, abort, a.status)) break;
       tmem_fence_after();
       const int cols = tl.cols();
       const int64_t col0 = a.gate ? static_cast<int64_t>(tl.f) * (kTileF / 2) + quad * 16
@@ -634,10 +698,25 @@ bool codes_map(CUtensorMap* m, const void* codes, int64_t rows, int32_t K, uint3
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// codes [E, 2, N/2, K/2] with the N/2 features in groups of 16: a box is four groups' gate and up features by 128
+// bytes, group by group
+bool gate_map(CUtensorMap* m, const void* codes, int32_t E, int32_t N, int32_t K) {
+  const EncodeTiled enc = encode_tiled();
+  if (enc == nullptr) return false;
+  const cuuint64_t row = static_cast<cuuint64_t>(K / 2);
+  const cuuint64_t dims[5] = {row, kBoxRows, 2, static_cast<cuuint64_t>(N / 2 / kBoxRows), static_cast<cuuint64_t>(E)};
+  const cuuint64_t strides[4] = {row, row * (N / 2), row * kBoxRows, row * N};
+  const cuuint32_t boxes[5] = {kStageK / 2, kBoxRows, 2, kTileF / 2 / kBoxRows, 1};
+  const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<void*>(codes), dims, strides, boxes, ones,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 constexpr int kPairRows = 64;  // rows an expert from which on pairs of CTAs take a tile
 
 template <int CG>
-moe_status_t launch_product(ProductArgs a, const CUtensorMap& mx, const CUtensorMap& mw, cudaStream_t st) {
+moe_status_t launch_product(ProductArgs a, const CUtensorMap (&mx)[3], const CUtensorMap& mw, cudaStream_t st) {
   const int per = CG * (a.gate ? kTileF / 2 : kTileF);
   a.ftiles = static_cast<int>((a.ld_out + per - 1) / per);
   const int sms = moe_host::sm_count();
@@ -664,7 +743,7 @@ moe_status_t launch_product(ProductArgs a, const CUtensorMap& mx, const CUtensor
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = CG == 1 ? 1 : 2;
-  return cudaLaunchKernelEx(&cfg, grouped_mx4_kernel<CG>, mx, mw, a) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, grouped_mx4_kernel<CG>, mx[0], mx[1], mx[2], mw, a) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // namespace
@@ -701,9 +780,12 @@ extern "C" moe_status_t moe_grouped_gemm_mx4(const void* x_codes, const void* x_
   a.capacity = capacity;
   a.out = static_cast<__nv_bfloat16*>(out);
   a.status = device_status;
-  CUtensorMap mx, mw;
-  if (!codes_map(&mx, x_codes, capacity, K, kBoxRows) ||
-      !codes_map(&mw, w_codes, static_cast<int64_t>(E_local) * N, K, gate ? kBoxRows : kTileF))
+  a.gate_box = gate && (N % 32) == 0 ? 1 : 0;
+  CUtensorMap mx[3], mw;
+  for (int i = 0; i < 3; ++i)
+    if (!codes_map(&mx[i], x_codes, capacity, K, kBoxRows << i)) return MOE_ERR_CUDA;
+  if (!(a.gate_box ? gate_map(&mw, w_codes, E_local, N, K)
+                   : codes_map(&mw, w_codes, static_cast<int64_t>(E_local) * N, K, gate ? kBoxRows : kTileF)))
     return MOE_ERR_CUDA;
   // many rows an expert: pairs of CTAs
   return capacity >= int64_t{E_local} * kPairRows ? launch_product<2>(a, mx, mw, static_cast<cudaStream_t>(stream))
