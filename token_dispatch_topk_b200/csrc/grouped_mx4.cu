@@ -16,7 +16,7 @@
 // 128 features and half of the rows, which halves what comes through L2 per product.
 //
 // The CTAs (one per SM) walk the tiles.  Warp 0: TMA loads into a ring of 256-element stages.  Warps 2 and 3: the
-// scale words of the stage's two 128-element chunks into the order tcgen05.cp wants, read ahead into registers.
+// scale words of the stage's two 128-element chunks, by four-byte copies into the order that tcgen05.cp wants.
 // Warp 1: copies the scales to TMEM and issues the products (kind::mxf4, block-scaled, 64 elements each; in a pair the
 // second CTA's warp 1 only tells the first that its stage is there).  Warps 4..11: the accumulator of the previous tile
 // out of TMEM, each warp its 32 lanes by every other 32 columns, transposed by stmatrix into rows of out.
@@ -39,7 +39,6 @@ constexpr int kAtom = 512;              // scales of 128 rows by 128 elements
 constexpr int kEpiT = 32;               // columns an epilogue warp takes at a time
 constexpr int kEpiStride = 32 + 8;      // bf16 a row of its transposed block (80 bytes: conflict-free)
 constexpr int kMaxExperts = 1024;
-constexpr int kSfAhead = 4;             // stages whose scales are in registers
 constexpr uint32_t kTmemCols = 512;
 
 template <int CG>  // CTAs a tile
@@ -113,6 +112,10 @@ __device__ __forceinline__ uint64_t desc_plain(uint32_t addr) {
          (uint64_t{1} << 46);
 }
 
+__device__ __forceinline__ void copy_word(uint8_t* dst, const uint32_t* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(moe::smem_addr(dst)), "l"(src) : "memory");
+}
+
 // 512 bytes of scales to four TMEM columns; in a pair, each CTA's own shared memory to its own TMEM.
 template <int CG>
 __device__ __forceinline__ void sf_to_tmem(uint32_t taddr, uint64_t smem_desc) {
@@ -154,34 +157,26 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
         : "memory");
 }
 
-// Arrive at CTA 0's barrier of the pair.
+// Arrive at CTA 0's barrier of the pair.  What it announces is in shared memory or TMEM, which have one copy, and was
+// complete before (the stage's own barrier, tcgen05.wait), so the release need not reach beyond the CTA: with
+// .release.cluster an arrival also waits for the CTA's global stores, about 1300 cycles, and bounded the whole kernel.
 __device__ __forceinline__ void arrive_first(uint64_t* bar) {
   asm volatile(
       "{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %0, 0;\n\t"
-      "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [r];\n\t}" ::"r"(moe::smem_addr(bar))
+      "mbarrier.arrive.shared::cluster.b64 _, [r];\n\t}" ::"r"(moe::smem_addr(bar))
       : "memory");
 }
 
-// Non-blocking test of a phase (kCluster: with the other CTA's writes before its arrival).
-template <bool kCluster>
+// Non-blocking test of a phase.
 __device__ __forceinline__ bool phase_done(uint64_t* bar, uint32_t parity) {
   uint32_t done;
-  if constexpr (kCluster)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(moe::smem_addr(bar)), "r"(parity)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(moe::smem_addr(bar)), "r"(parity)
-        : "memory");
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(moe::smem_addr(bar)), "r"(parity)
+      : "memory");
   return done != 0u;
 }
 __device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -214,13 +209,12 @@ __device__ __forceinline__ float silu_times(uint32_t gate, uint32_t up) {
 // A bounded wait of a warp; it also gives up when another role of the CTA has.  The first test is inline and its vote
 // uniform, so that the loops around it stay convergent: the issuing warps must not run as a lone lane, whose operands
 // go one by one through vector registers (1675 cycles to issue a stage that takes 450 to compute).
-template <bool kCluster>
 __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* status) {
   uint64_t t0 = 0;
   for (;;) {
 #pragma unroll 1
     for (int i = 0; i < 256; ++i)
-      if (phase_done<kCluster>(bar, parity)) return true;
+      if (phase_done(bar, parity)) return true;
     if (*abort != 0) return false;
     const uint64_t t = moe::global_ns();
     if (t0 == 0) t0 = t;
@@ -231,10 +225,17 @@ __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile 
     }
   }
 }
-template <bool kCluster = false>
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* status) {
-  if (__all_sync(0xffffffffu, phase_done<kCluster>(bar, parity))) return true;
-  return __all_sync(0xffffffffu, wait_slow<kCluster>(bar, parity, abort, status));
+  if (__all_sync(0xffffffffu, phase_done(bar, parity))) return true;
+  return __all_sync(0xffffffffu, wait_slow(bar, parity, abort, status));
+}
+
+// Two of them, their first tests in flight together.
+__device__ __forceinline__ bool wait_both(uint64_t* bar, uint32_t parity, uint64_t* bar2, uint32_t parity2,
+                                          volatile int* abort, int32_t* status) {
+  const bool one = phase_done(bar, parity), two = bar2 == nullptr || phase_done(bar2, parity2);
+  if (__all_sync(0xffffffffu, one && two)) return true;
+  return wait_warp(bar, parity, abort, status) && (bar2 == nullptr || wait_warp(bar2, parity2, abort, status));
 }
 
 // One lane of a converged warp, always the same.
@@ -315,8 +316,8 @@ grouped_mx4_kernel(const __grid_constant__ CUtensorMap map_x16, const __grid_con
   const int rank = CG == 1 ? 0 : blockIdx.x % CG;  // in the pair
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
-      // the TMA warp and the two scale warps; in a pair, at the first CTA, the second's stage too
-      moe::mbar_init(&s.full[i], CG == 2 && rank == 0 ? 4 : 3);
+      // the TMA warp and the lanes of the two scale warps; in a pair, at the first CTA, the second's stage too
+      moe::mbar_init(&s.full[i], CG == 2 && rank == 0 ? 66 : 65);
       moe::mbar_init(&s.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -448,25 +449,25 @@ grouped_mx4_kernel(const __grid_constant__ CUtensorMap map_x16, const __grid_con
     uint32_t round = 0, buf = 0, buf_round = 0, set = 0;
     int st2 = 0;  // the stage two before this one, and its round
     uint32_t round2 = 0;
-    bool first = true, second = false, ok = true;
+    int before = 0;  // stages before this one, up to 2
+    bool ok = true;
     while (ok && tl.next()) {
-      if (!wait_warp<CG == 2>(&s.acc_empty[buf], (buf_round & 1u) ^ 1u, abort, a.status)) break;
+      if (!wait_warp(&s.acc_empty[buf], (buf_round & 1u) ^ 1u, abort, a.status)) break;
       tmem_fence_after();
       const uint32_t idesc = kDesc | ((static_cast<uint32_t>(tl.cols()) >> 3) << 17);
       const uint32_t d = tmem + buf * S::kTileT;
       for (int kb = 0; kb < a.kstages; ++kb) {
-        bool here = wait_warp<CG == 2>(&s.full[st], round & 1u, abort, a.status);
-        // the products that read this set of TMEM scales, two stages ago, are done
-        if (!first && !second) {
-          here = here && wait_warp(&s.empty[st2], round2 & 1u, abort, a.status);
-          if (++st2 == kStages) { st2 = 0; ++round2; }
-        }
-        second = first;
-        first = false;
-        if (!here) {
+        // the stage is there, and the products that read this set of TMEM scales, two stages ago, are done
+        if (!wait_both(&s.full[st], round & 1u, before < 2 ? nullptr : &s.empty[st2], round2 & 1u, abort, a.status)) {
           ok = false;
           break;
         }
+        if (before == 2) {
+          if (++st2 == kStages) { st2 = 0; ++round2; }
+        } else {
+          ++before;
+        }
+        moe::fence_proxy_async_smem();  // the scales were written by ordinary copies
         tmem_fence_after();
         if (elect_one()) {
           const uint32_t sf = tmem + S::kTmemSf + set * S::kSfCols;
@@ -505,82 +506,67 @@ grouped_mx4_kernel(const __grid_constant__ CUtensorMap map_x16, const __grid_con
           ok = false;
           break;
         }
+        moe::fence_proxy_async_smem();  // the scales were written by ordinary copies
         if (elect_one()) arrive_first(&s.full[st]);
         __syncwarp();
         if (++st == kStages) { st = 0; ++round; }
       }
     }
   } else if (warp < 4) {
-    // scales: chunk 2 kb + (warp - 2) of each stage, for lane l the words of rows l, 32 + l, 64 + l, 96 + l
+    // Scales: chunk 2 kb + (warp - 2) of each stage.  Lane l copies the words of rows l, 32 + l, 64 + l, 96 + l (of the
+    // weights' tile, then of each 128 of x's) side by side; the copies (cp.async) complete on the stage's barrier.
     Tiles<CG> tl(a, s.first_tile);
-    // (nothing is computed from a word before its stage's turn: the loads stay in flight)
-    constexpr uint32_t kOne = 0x7f7f7f7fu;
     const int which = warp - 2;
-    int kb = 0, kb_st = 0;
-    // bytes of blocks past K in the last chunk: 1, whatever is there (the codes are zeros, but NaN times zero is NaN)
-    const int past = a.chunks * 4 - a.K / 32;
-    const uint32_t keep_last = past > 0 ? 0xffffffffu >> (8 * past) : 0xffffffffu;
-    bool more = tl.next();
-    uint4 va[kSfAhead], vb[kSfAhead][S::kAtomsB];
-    bool have[kSfAhead];
     const int64_t w_rows = static_cast<int64_t>(a.E) * a.N;
-    auto load = [&](int i) {
-      have[i] = more;
-      if (!more) return;
-      const int c = kb * 2 + which;
-      va[i] = make_uint4(kOne, kOne, kOne, kOne);
-#pragma unroll
-      for (int h = 0; h < S::kAtomsB; ++h) vb[i][h] = va[i];
-      if (c < a.chunks) {
-        const uint32_t* w = a.w_sf + c * w_rows;
-        va[i] = make_uint4(__ldg(w + tl.weight_row(lane)), __ldg(w + tl.weight_row(lane + 32)),
-                           __ldg(w + tl.weight_row(lane + 64)), __ldg(w + tl.weight_row(lane + 96)));
-        const uint32_t* x = a.x_sf + c * a.capacity;
-        auto word = [&](int n) -> uint32_t { return n < tl.rows ? __ldg(x + tl.row0 + n) : kOne; };
-#pragma unroll
-        for (int h = 0; h < S::kAtomsB; ++h)
-          vb[i][h] = make_uint4(word(h * 128 + lane), word(h * 128 + 32 + lane), word(h * 128 + 64 + lane),
-                                word(h * 128 + 96 + lane));
-      }
-      if (++kb == a.kstages) {
-        kb = 0;
-        more = tl.next();
-      }
-    };
-#pragma unroll
-    for (int i = 0; i < kSfAhead; ++i) load(i);
     int st = 0;
     uint32_t round = 0;
     bool ok = true;
-    while (ok) {
+    while (ok && tl.next()) {
+      const int groups = (tl.cols() + 31) / 32;
+      int wr[4], xr[4 * S::kAtomsB];
 #pragma unroll
-      for (int i = 0; i < kSfAhead; ++i) {
-        if (!ok || !have[i]) {
-          ok = false;
-          continue;
-        }
+      for (int c = 0; c < 4; ++c) wr[c] = static_cast<int>(tl.weight_row(32 * c + lane));
+#pragma unroll
+      for (int c = 0; c < 4 * S::kAtomsB; ++c) {  // (columns past the rows repeat the last one: not stored)
+        const int n = 32 * c + lane;
+        xr[c] = tl.row0 + (n < tl.rows ? n : tl.rows - 1);
+      }
+      const uint32_t* w = a.w_sf + which * w_rows;
+      const uint32_t* x = a.x_sf + which * a.capacity;
+      for (int kb = 0; kb < a.kstages; ++kb, w += 2 * w_rows, x += 2 * a.capacity) {
         if (!wait_warp(&s.empty[st], (round & 1u) ^ 1u, abort, a.status)) {
           ok = false;
-          continue;
+          break;
         }
-        const uint32_t keep = kb_st * 2 + which == a.chunks - 1 ? keep_last : 0xffffffffu;
-        if (++kb_st == a.kstages) kb_st = 0;
-        auto put = [&](uint8_t* dst, const uint4& v) {
-          const uint32_t one = kOne & ~keep;
-          *reinterpret_cast<uint4*>(dst + lane * 16) =
-              make_uint4((v.x & keep) | one, (v.y & keep) | one, (v.z & keep) | one, (v.w & keep) | one);
-        };
-        uint8_t* sf = s.sf[st];
-        put(sf + which * kAtom, va[i]);
+        uint8_t* sfa = s.sf[st] + which * kAtom + lane * 16;
+        uint8_t* sfb = s.sf[st] + (2 + which * S::kAtomsB) * kAtom + lane * 16;
+        if ((kb + 1) * kStageK <= a.K) {
 #pragma unroll
-        for (int h = 0; h < S::kAtomsB; ++h) put(sf + 2 * kAtom + (which * S::kAtomsB + h) * kAtom, vb[i][h]);
-        moe::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) moe::mbar_arrive(&s.full[st]);
+          for (int c = 0; c < 4; ++c) copy_word(sfa + 4 * c, w + wr[c]);
+#pragma unroll
+          for (int c = 0; c < 4 * S::kAtomsB; ++c)
+            if (c < groups) copy_word(sfb + (c >> 2) * kAtom + 4 * (c & 3), x + xr[c]);
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(moe::smem_addr(&s.full[st]))
+                       : "memory");
+        } else {  // the last stage of a K that is no multiple of 256
+          // bytes of blocks past K: 1, whatever is there (their codes are zeros, but NaN times zero is NaN)
+          const int c0 = 2 * kb + which, past = (c0 + 1) * 4 - a.K / 32;
+          const uint32_t keep = past <= 0 ? 0xffffffffu : past >= 4 ? 0u : 0xffffffffu >> (8 * past);
+          auto put = [&](uint8_t* dst, const uint32_t* src) {
+            *reinterpret_cast<uint32_t*>(dst) = ((keep != 0u ? __ldg(src) : 0u) & keep) | (0x7f7f7f7fu & ~keep);
+          };
+#pragma unroll
+          for (int c = 0; c < 4; ++c) put(sfa + 4 * c, w + wr[c]);
+#pragma unroll
+          for (int c = 0; c < 4 * S::kAtomsB; ++c)
+            if (c < groups) put(sfb + (c >> 2) * kAtom + 4 * (c & 3), x + xr[c]);
+          moe::fence_proxy_async_smem();
+          moe::mbar_arrive(&s.full[st]);
+        }
         if (++st == kStages) { st = 0; ++round; }
-        load(i);
       }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
     Tiles<CG> tl(a, s.first_tile);
     const int quad = warp & 3, turn = (warp - 4) >> 2;  // lanes 32 quad .. +31, column blocks turn, turn + 2, ...
