@@ -33,7 +33,7 @@ constexpr int kThreads = 384;
 constexpr int kEpiWarps = 8;
 constexpr int kTileF = 128;             // features a CTA and tile
 constexpr int kStageK = 256;            // elements of K a stage: 128 bytes, one swizzle atom
-constexpr int kBoxRows = 16;            // rows of x in TMA boxes of 16, 32 and 64; gate features before the up ones
+constexpr int kBoxRows = 16;            // rows of the smallest TMA box of x; gate features before the up ones
 constexpr int kBytesA = kTileF * kStageK / 2;
 constexpr int kAtom = 512;              // scales of 128 rows by 128 elements
 constexpr int kEpiT = 32;               // columns an epilogue warp takes at a time
@@ -245,57 +245,63 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0u;
 }
 
-// The tiles of this CTA (or pair), in order: expert by expert, then row tiles, features fastest.  The next tile's
-// count and offset are read one tile ahead (a first use costs an L2 round trip).
+// Tile t: its first row, and 10 bits of expert, 8 of rows, 13 of feature tile.  (By value, not a method: a struct whose
+// address is taken lives in local memory.)
+template <int CG>
+__device__ __noinline__ int2 tile_of(int t, const int32_t* first, const int32_t* counts, const int32_t* offsets, int E,
+                                     int ftiles) {
+  const int rt = t / ftiles, ft = t - rt * ftiles;
+  int lo = 0, hi = E - 1;  // the last expert with first[] <= rt: one that has rows
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (first[mid] <= rt) lo = mid;
+    else hi = mid - 1;
+  }
+  const int cnt = counts[lo], n = first[lo + 1] - first[lo], i = rt - first[lo];
+  constexpr int kStep = Shape<CG>::kStepT;
+  const int per = ((cnt + n - 1) / n + kStep - 1) / kStep * kStep;  // at most kTileT
+  return make_int2(offsets[lo] + i * per, (lo << 21) | ((cnt - i * per < per ? cnt - i * per : per) << 13) | ft);
+}
+
+// The tiles of this CTA (or pair), in order: expert by expert, then row tiles, features fastest.  The lanes of a warp
+// work out 32 tiles at a time (a search, a division and two loads each, over 1000 cycles), which next() passes round.
 template <int CG>
 struct Tiles {
   const ProductArgs& a;
   const int32_t* first;  // row tiles before expert e
-  int e = 0;
-  int f, row0, rows;  // this CTA's feature tile, the tile's first row, its rows
-  int rt, ft, step_rt, step_ft;     // the next tile: row tile, feature tile; and the stride between this CTA's tiles
-  int next_e = 0, next_cnt, next_off;
+  int e, f, row0, rows;  // expert, this CTA's feature tile, the tile's first row, its rows
+  int at, total;         // the next tile, and all
+  int turn = 32;         // lane that holds the next tile
+  int2 mine;             // this lane's tile
 
-  __device__ Tiles(const ProductArgs& args, const int32_t* first_tile) : a(args), first(first_tile) {
-    const int at = blockIdx.x / CG, stride = gridDim.x / CG;
-    rt = at / a.ftiles;
-    ft = at - rt * a.ftiles;
-    step_rt = stride / a.ftiles;
-    step_ft = stride - step_rt * a.ftiles;
-    ahead();
-  }
-  __device__ void ahead() {
-    if (rt >= first[a.E]) return;
-    while (first[next_e + 1] <= rt) ++next_e;
-    next_cnt = a.counts[next_e];
-    next_off = a.offsets[next_e];
-  }
-  __device__ bool next() {
-    if (rt >= first[a.E]) return false;
-    e = next_e;
-    f = ft * CG + (CG == 1 ? 0 : blockIdx.x % CG);
-    const int n = first[e + 1] - first[e], i = rt - first[e];
-    constexpr int kStep = Shape<CG>::kStepT;
-    const int per = ((next_cnt + n - 1) / n + kStep - 1) / kStep * kStep;  // at most kTileT
-    row0 = next_off + i * per;
-    rows = next_cnt - i * per < per ? next_cnt - i * per : per;
-    rt += step_rt;
-    ft += step_ft;
-    if (ft >= a.ftiles) {
-      ft -= a.ftiles;
-      ++rt;
+  __device__ __forceinline__ Tiles(const ProductArgs& args, const int32_t* first_tile)
+      : a(args), first(first_tile), at(blockIdx.x / CG), total(first_tile[args.E] * args.ftiles) {}
+  __device__ __forceinline__ bool next() {
+    if (at >= total) return false;
+    if (turn == 32) {
+      const int t = at + static_cast<int>(threadIdx.x & 31) * static_cast<int>(gridDim.x / CG);
+      mine = make_int2(0, 0);
+      if (t < total) mine = tile_of<CG>(t, first, a.counts, a.offsets, a.E, a.ftiles);
+      __syncwarp();
+      turn = 0;
     }
-    ahead();
+    row0 = __shfl_sync(0xffffffffu, mine.x, turn);
+    const int v = __shfl_sync(0xffffffffu, mine.y, turn);
+    e = v >> 21;
+    rows = (v >> 13) & 255;
+    f = (v & 8191) * CG + (CG == 1 ? 0 : blockIdx.x % CG);
+    ++turn;
+    at += gridDim.x / CG;
     return true;
   }
   // the product's columns
-  __device__ int cols() const { return (rows + Shape<CG>::kStepT - 1) / Shape<CG>::kStepT * Shape<CG>::kStepT; }
+  __device__ __forceinline__ int cols() const { return (rows + Shape<CG>::kStepT - 1) / Shape<CG>::kStepT * Shape<CG>::kStepT; }
   // the first weight row of the tile (with the gate: of its gate features)
-  __device__ int64_t weight_row0() const {
+  __device__ __forceinline__ int64_t weight_row0() const {
     return static_cast<int64_t>(e) * a.N + static_cast<int64_t>(f) * (a.gate ? kTileF / 2 : kTileF);
   }
   // row of the weights that lane m of the tile holds (clamped: lanes past the expert's features are not stored)
-  __device__ int64_t weight_row(int m) const {
+  __device__ __forceinline__ int64_t weight_row(int m) const {
     const int64_t r = weight_row0() + (!a.gate ? m : (m & 16 ? a.N / 2 : 0) + (m >> 5) * 16 + (m & 15));
     const int64_t last = static_cast<int64_t>(a.E) * a.N - 1;
     return r < last ? r : last;
@@ -305,8 +311,8 @@ struct Tiles {
 template <int CG>
 __global__ void __launch_bounds__(kThreads, 1)
 grouped_mx4_kernel(const __grid_constant__ CUtensorMap map_x16, const __grid_constant__ CUtensorMap map_x32,
-                   const __grid_constant__ CUtensorMap map_x64, const __grid_constant__ CUtensorMap map_w,
-                   const ProductArgs a) {
+                   const __grid_constant__ CUtensorMap map_x64, const __grid_constant__ CUtensorMap map_x,
+                   const __grid_constant__ CUtensorMap map_w, const ProductArgs a) {
   using S = Shape<CG>;
   constexpr int kStages = S::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -397,6 +403,9 @@ grouped_mx4_kernel(const __grid_constant__ CUtensorMap map_x16, const __grid_con
     bool ok = true;
     while (ok && tl.next()) {
       const int half = tl.cols() / CG;  // columns whose rows this CTA loads
+      // ... in one box, which may be a little higher: a box costs the issuing warp about 100 cycles, rows little
+      const int box = half <= 16 ? 16 : half <= 32 ? 32 : half <= 64 ? 64 : S::kRowsB;
+      const CUtensorMap* map = half <= 16 ? &map_x16 : half <= 32 ? &map_x32 : half <= 64 ? &map_x64 : &map_x;
       const int wr = static_cast<int>(tl.weight_row0()), up = a.N / 2;
       const int xr = tl.row0 + rank * half;
       for (int kb = 0; kb < a.kstages; ++kb) {
@@ -405,7 +414,7 @@ grouped_mx4_kernel(const __grid_constant__ CUtensorMap map_x16, const __grid_con
           break;
         }
         if (elect_one()) {
-          moe::mbar_arrive_expect_tx(&s.full[st], kBytesA + half * 128);
+          moe::mbar_arrive_expect_tx(&s.full[st], kBytesA + box * 128);
           const int x = kb * 128;
           uint8_t* dst = s.ab[st];
           if (!a.gate) {
@@ -419,17 +428,7 @@ grouped_mx4_kernel(const __grid_constant__ CUtensorMap map_x16, const __grid_con
               tma_load_2d(dst + (2 * b + 1) * kBoxRows * 128, &map_w, x, wr + up + b * kBoxRows, &s.full[st]);
             }
           }
-          dst += kBytesA;  // then the rows, in the fewest boxes: each costs the copy engine about 70 cycles
-          int done = 0;
-          if (half & 64) {
-            tma_load_2d(dst, &map_x64, x, xr, &s.full[st]);
-            done = 64;
-          }
-          if (half & 32) {
-            tma_load_2d(dst + done * 128, &map_x32, x, xr + done, &s.full[st]);
-            done += 32;
-          }
-          if (half & 16) tma_load_2d(dst + done * 128, &map_x16, x, xr + done, &s.full[st]);
+          tma_load_2d(dst + kBytesA, map, x, xr, &s.full[st]);
         }
         __syncwarp();
         ++issued;
@@ -702,7 +701,7 @@ bool gate_map(CUtensorMap* m, const void* codes, int32_t E, int32_t N, int32_t K
 constexpr int kPairRows = 64;  // rows an expert from which on pairs of CTAs take a tile
 
 template <int CG>
-moe_status_t launch_product(ProductArgs a, const CUtensorMap (&mx)[3], const CUtensorMap& mw, cudaStream_t st) {
+moe_status_t launch_product(ProductArgs a, const CUtensorMap (&mx)[4], const CUtensorMap& mw, cudaStream_t st) {
   const int per = CG * (a.gate ? kTileF / 2 : kTileF);
   a.ftiles = static_cast<int>((a.ld_out + per - 1) / per);
   const int sms = moe_host::sm_count();
@@ -729,7 +728,7 @@ moe_status_t launch_product(ProductArgs a, const CUtensorMap (&mx)[3], const CUt
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = CG == 1 ? 1 : 2;
-  return cudaLaunchKernelEx(&cfg, grouped_mx4_kernel<CG>, mx[0], mx[1], mx[2], mw, a) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, grouped_mx4_kernel<CG>, mx[0], mx[1], mx[2], mx[3], mw, a) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // namespace
@@ -767,13 +766,15 @@ extern "C" moe_status_t moe_grouped_gemm_mx4(const void* x_codes, const void* x_
   a.out = static_cast<__nv_bfloat16*>(out);
   a.status = device_status;
   a.gate_box = gate && (N % 32) == 0 ? 1 : 0;
-  CUtensorMap mx[3], mw;
-  for (int i = 0; i < 3; ++i)
-    if (!codes_map(&mx[i], x_codes, capacity, K, kBoxRows << i)) return MOE_ERR_CUDA;
+  const bool pair = capacity >= int64_t{E_local} * kPairRows;  // many rows an expert
+  CUtensorMap mx[4], mw;
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t box = i < 3 ? kBoxRows << i : pair ? Shape<2>::kRowsB : Shape<1>::kRowsB;
+    if (!codes_map(&mx[i], x_codes, capacity, K, box)) return MOE_ERR_CUDA;
+  }
   if (!(a.gate_box ? gate_map(&mw, w_codes, E_local, N, K)
                    : codes_map(&mw, w_codes, static_cast<int64_t>(E_local) * N, K, gate ? kBoxRows : kTileF)))
     return MOE_ERR_CUDA;
-  // many rows an expert: pairs of CTAs
-  return capacity >= int64_t{E_local} * kPairRows ? launch_product<2>(a, mx, mw, static_cast<cudaStream_t>(stream))
-                                                  : launch_product<1>(a, mx, mw, static_cast<cudaStream_t>(stream));
+  return pair ? launch_product<2>(a, mx, mw, static_cast<cudaStream_t>(stream))
+              : launch_product<1>(a, mx, mw, static_cast<cudaStream_t>(stream));
 }
