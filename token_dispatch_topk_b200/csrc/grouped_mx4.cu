@@ -37,7 +37,7 @@ constexpr int kBoxRows = 16;            // rows of the smallest TMA box of x; ga
 constexpr int kBytesA = kTileF * kStageK / 2;
 constexpr int kAtom = 512;              // scales of 128 rows by 128 elements
 constexpr int kEpiT = 32;               // columns an epilogue warp takes at a time
-constexpr int kEpiStride = 32 + 8;      // bf16 a row of its transposed block (80 bytes: conflict-free)
+constexpr int kEpiBytes = kEpiT * 64;   // its transposed block: rows of 32 (with the gate 16) bf16, swizzled
 constexpr int kMaxExperts = 1024;
 constexpr uint32_t kTmemCols = 512;
 
@@ -45,7 +45,7 @@ template <int CG>  // CTAs a tile
 struct Shape {
   static constexpr int kTileT = CG == 1 ? 64 : 224;  // rows a tile, at most
   static constexpr int kStepT = CG == 1 ? 16 : 32;   // columns of a product: a multiple of this
-  static constexpr int kStages = CG == 1 ? 7 : 6;
+  static constexpr int kStages = CG == 1 ? 7 : 5;
   static constexpr int kRowsB = kTileT / CG;         // rows of x a CTA loads
   static constexpr int kBytesB = kRowsB * kStageK / 2;
   static constexpr int kStageBytes = kBytesA + kBytesB;
@@ -60,7 +60,7 @@ struct Shape {
   struct __align__(1024) Smem {
     uint8_t ab[kStages][kStageBytes];  // A then B, 128-byte swizzled
     uint8_t sf[kStages][kBytesSf];     // A's two atoms, then B's, chunk by chunk
-    __nv_bfloat16 epi[kEpiWarps][kEpiT * kEpiStride];
+    uint8_t epi[kEpiWarps][2][kEpiBytes];
     int32_t first_tile[kMaxExperts + 1];  // row tiles before expert e
     int32_t warp_sums[kThreads / 32];
     uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drained;
@@ -312,7 +312,8 @@ template <int CG>
 __global__ void __launch_bounds__(kThreads, 1)
 grouped_mx4_kernel(const __grid_constant__ CUtensorMap map_x16, const __grid_constant__ CUtensorMap map_x32,
                    const __grid_constant__ CUtensorMap map_x64, const __grid_constant__ CUtensorMap map_x,
-                   const __grid_constant__ CUtensorMap map_w, const ProductArgs a) {
+                   const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_out,
+                   const ProductArgs a) {
   using S = Shape<CG>;
   constexpr int kStages = S::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -569,25 +570,26 @@ grouped_mx4_kernel(const __grid_constant__ CUtensorMap map_x16, const __grid_con
   } else {
     Tiles<CG> tl(a, s.first_tile);
     const int quad = warp & 3, turn = (warp - 4) >> 2;  // lanes 32 quad .. +31, column blocks turn, turn + 2, ...
-    __nv_bfloat16* epi = s.epi[warp - 4];
-    const uint32_t epi_addr = moe::smem_addr(epi);
-    uint32_t buf = 0, buf_round = 0;
+    uint32_t buf = 0, buf_round = 0, half = 0;
+    // a lane's place in a block: stmatrix writes 16 bytes of row j at chunk m, both swizzled as the store's map says
+    const int sj = lane & 7, sm = lane >> 3;
     while (tl.next()) {
       if (!wait_warp(&s.acc_full[buf], buf_round & 1u, abort, a.status)) break;
       tmem_fence_after();
       const int cols = tl.cols();
-      const int64_t col0 = a.gate ? static_cast<int64_t>(tl.f) * (kTileF / 2) + quad * 16
-                                  : static_cast<int64_t>(tl.f) * kTileF + quad * 32;
+      const int col0 = a.gate ? tl.f * (kTileF / 2) + quad * 16 : tl.f * kTileF + quad * 32;
       for (int c0 = turn * kEpiT; c0 < cols; c0 += 2 * kEpiT) {
         uint32_t lo[16], hi[16];  // lanes 0..15 and 16..31: with the gate, gate and up
         const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * S::kTileT + c0;
         tmem_ld16x32(taddr, lo);
         tmem_ld16x32(taddr + (16u << 16), hi);
+        uint8_t* epi = s.epi[warp - 4][half];
+        const uint32_t epi_addr = moe::smem_addr(epi);
+        half ^= 1u;
+        if (elect_one()) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");  // this half has been read
+        __syncwarp();
         tmem_wait_ld();
-        __syncwarp();  // the previous block has been read
-        const int left = tl.rows - c0 < kEpiT ? tl.rows - c0 : kEpiT;
-        __nv_bfloat16* out = a.out + static_cast<int64_t>(tl.row0 + c0) * a.ld_out + col0;
-        if (a.gate) {  // 16 features: 32 bytes a row
+        if (a.gate) {  // 16 features, rows of 32 bytes: chunk ^= row / 4
 #pragma unroll
           for (int i = 0; i < 4; i += 2) {
             uint32_t p[4];
@@ -597,35 +599,43 @@ grouped_mx4_kernel(const __grid_constant__ CUtensorMap map_x16, const __grid_con
               p[q] = moe::pack_bf16x2(silu_times(lo[v], hi[v]), silu_times(lo[v + 1], hi[v + 1]));
             }
             // blocks: columns 8i, features 0..7 and 8..15; columns 8i + 8, the same
-            const int row = 8 * (i + (lane >> 4)) + (lane & 7);
-            stmatrix_trans(epi_addr + row * (kEpiStride * 2) + ((lane >> 3) & 1) * 16, p[0], p[1], p[2], p[3]);
+            stmatrix_trans(epi_addr + (8 * (i + (sm >> 1)) + sj) * 32 + (((sm & 1) ^ (sj >> 2)) << 4), p[0], p[1], p[2],
+                           p[3]);
           }
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int j = i * 16 + (lane >> 1), g = (lane & 1) * 8;
-            const uint4 v = moe::lds128(epi + j * kEpiStride + g);
-            if (j < left && col0 + g < a.ld_out)
-              moe::st_plain(reinterpret_cast<uint4*>(out + j * a.ld_out + g), v);
-          }
-        } else {  // 32 features: 64 bytes a row
+        } else {  // 32 features, rows of 64 bytes: chunk ^= row / 2
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int v = 4 * i;
-            stmatrix_trans(epi_addr + (8 * i + (lane & 7)) * (kEpiStride * 2) + (lane >> 3) * 16,
+            stmatrix_trans(epi_addr + (8 * i + sj) * 64 + ((sm ^ (sj >> 1)) << 4),
                            moe::pack_bf16x2(__uint_as_float(lo[v]), __uint_as_float(lo[v + 1])),
                            moe::pack_bf16x2(__uint_as_float(lo[v + 2]), __uint_as_float(lo[v + 3])),
                            moe::pack_bf16x2(__uint_as_float(hi[v]), __uint_as_float(hi[v + 1])),
                            moe::pack_bf16x2(__uint_as_float(hi[v + 2]), __uint_as_float(hi[v + 3])));
           }
+        }
+        const int left = tl.rows - c0;
+        if (left >= kEpiT) {  // whole: one copy (features past the last are clipped)
+          moe::fence_proxy_async_smem();
           __syncwarp();
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int j = i * 8 + (lane >> 2), g = (lane & 3) * 8;
-            const uint4 v = moe::lds128(epi + j * kEpiStride + g);
-            if (j < left && col0 + g < a.ld_out)
-              moe::st_plain(reinterpret_cast<uint4*>(out + j * a.ld_out + g), v);
+          if (elect_one()) {
+            if (col0 < a.ld_out)
+              asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                               &map_out),
+                           "r"(col0), "r"(tl.row0 + c0), "r"(epi_addr)
+                           : "memory");
+            moe::bulk_commit();
           }
+        } else {  // the last rows of an expert: what follows is not this expert's to write
+          __syncwarp();
+          __nv_bfloat16* out = a.out + static_cast<int64_t>(tl.row0 + c0) * a.ld_out + col0;
+          const int shift = a.gate ? 1 : 2;  // log2 of a row's 16-byte chunks
+          for (int i = lane; i < left << shift; i += 32) {
+            const int j = i >> shift, g = i & ((1 << shift) - 1);
+            if (col0 + g * 8 >= a.ld_out) continue;
+            const int at = a.gate ? j * 32 + ((g ^ ((j >> 2) & 1)) << 4) : j * 64 + ((g ^ ((j >> 1) & 3)) << 4);
+            moe::st_plain(reinterpret_cast<uint4*>(out + j * a.ld_out + g * 8), moe::lds128(epi + at));
+          }
+          if (elect_one()) moe::bulk_commit();  // (empty: a group a block)
         }
       }
       tmem_fence_before();
@@ -638,6 +648,8 @@ grouped_mx4_kernel(const __grid_constant__ CUtensorMap map_x16, const __grid_con
       }
       if (++buf == 2) { buf = 0; ++buf_round; }
     }
+    __syncwarp();
+    if (elect_one()) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
   tmem_fence_before();
   __syncthreads();
@@ -698,10 +710,24 @@ bool gate_map(CUtensorMap* m, const void* codes, int32_t E, int32_t N, int32_t K
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// out [capacity, cols] bf16: a box is 32 rows of an epilogue warp's 32 features, 16 with the gate
+bool out_map(CUtensorMap* m, void* out, int64_t rows, int64_t cols, bool gate) {
+  const EncodeTiled enc = encode_tiled();
+  if (enc == nullptr) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * 2};
+  const cuuint32_t boxes[2] = {gate ? 16u : 32u, kEpiT};
+  const cuuint32_t ones[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, out, dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             gate ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 constexpr int kPairRows = 64;  // rows an expert from which on pairs of CTAs take a tile
 
 template <int CG>
-moe_status_t launch_product(ProductArgs a, const CUtensorMap (&mx)[4], const CUtensorMap& mw, cudaStream_t st) {
+moe_status_t launch_product(ProductArgs a, const CUtensorMap (&mx)[4], const CUtensorMap& mw,
+                            const CUtensorMap& mo, cudaStream_t st) {
   const int per = CG * (a.gate ? kTileF / 2 : kTileF);
   a.ftiles = static_cast<int>((a.ld_out + per - 1) / per);
   const int sms = moe_host::sm_count();
@@ -728,7 +754,7 @@ moe_status_t launch_product(ProductArgs a, const CUtensorMap (&mx)[4], const CUt
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = CG == 1 ? 1 : 2;
-  return cudaLaunchKernelEx(&cfg, grouped_mx4_kernel<CG>, mx[0], mx[1], mx[2], mx[3], mw, a) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, grouped_mx4_kernel<CG>, mx[0], mx[1], mx[2], mx[3], mw, mo, a) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // namespace
@@ -767,7 +793,8 @@ extern "C" moe_status_t moe_grouped_gemm_mx4(const void* x_codes, const void* x_
   a.status = device_status;
   a.gate_box = gate && (N % 32) == 0 ? 1 : 0;
   const bool pair = capacity >= int64_t{E_local} * kPairRows;  // many rows an expert
-  CUtensorMap mx[4], mw;
+  CUtensorMap mx[4], mw, mo;
+  if (!out_map(&mo, out, capacity, a.ld_out, gate)) return MOE_ERR_CUDA;
   for (int i = 0; i < 4; ++i) {
     const uint32_t box = i < 3 ? kBoxRows << i : pair ? Shape<2>::kRowsB : Shape<1>::kRowsB;
     if (!codes_map(&mx[i], x_codes, capacity, K, box)) return MOE_ERR_CUDA;
@@ -775,6 +802,6 @@ extern "C" moe_status_t moe_grouped_gemm_mx4(const void* x_codes, const void* x_
   if (!(a.gate_box ? gate_map(&mw, w_codes, E_local, N, K)
                    : codes_map(&mw, w_codes, static_cast<int64_t>(E_local) * N, K, gate ? kBoxRows : kTileF)))
     return MOE_ERR_CUDA;
-  return pair ? launch_product<2>(a, mx, mw, static_cast<cudaStream_t>(stream))
-              : launch_product<1>(a, mx, mw, static_cast<cudaStream_t>(stream));
+  return pair ? launch_product<2>(a, mx, mw, mo, static_cast<cudaStream_t>(stream))
+              : launch_product<1>(a, mx, mw, mo, static_cast<cudaStream_t>(stream));
 }
