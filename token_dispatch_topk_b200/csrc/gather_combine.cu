@@ -179,7 +179,7 @@ constexpr uint32_t kCombineRingTarget = 64u * 1024u;   // bytes of stages per CT
 
 struct CombineArgs {
   const uint8_t* y;         // expert_out [capacity, H] bf16
-  const float* w;           // [T, k], or null for weights of 1
+  const float* w;           // [T, k]
   const int32_t* inv_perm;  // [T*k]
   int64_t T;
   int k;
@@ -243,7 +243,7 @@ __global__ void __launch_bounds__((1 + kCombineConsumerWarps) * 32) combine_tma_
       if (lane < spu && t < a.T) {
         const int64_t s = t * k + lane % k;
         r = a.inv_perm[s];
-        w = a.w == nullptr ? 1.f : a.w[s];
+        w = a.w[s];
         if (r < -1 || static_cast<int64_t>(r) >= a.capacity) {
           moe::record_status(a.status, MOE_ERR_BAD_ROW);
           r = -1;
@@ -403,7 +403,7 @@ combine_small_kernel(const uint4* __restrict__ y, const float* __restrict__ w, c
     float wj = 0.f;
     if (j0 + lane < k) {
       r = inv_perm[t * k + j0 + lane];
-      wj = w == nullptr ? 1.f : w[t * k + j0 + lane];
+      wj = w[t * k + j0 + lane];
       if (r < -1 || static_cast<int64_t>(r) >= capacity) {
         moe::record_status(status, MOE_ERR_BAD_ROW);
         r = -1;
@@ -524,17 +524,16 @@ extern "C" moe_status_t moe_gather(const void* hidden, int64_t T, int32_t H, int
   return MOE_OK;
 }
 
-// The sum of the tokens' rows, weighted (moe_combine) or not (moe_gather_backward: fmaf(1, y, acc) is y + acc).
-static moe_status_t combine_rows(const void* expert_out, const float* topk_weights, const int32_t* inv_perm,
-                                 int64_t T, int32_t k, int32_t H, int64_t capacity, void* out,
-                                 int32_t* device_status, void* stream) {
+extern "C" moe_status_t moe_combine(const void* expert_out, const float* topk_weights, const int32_t* inv_perm,
+                                    int64_t T, int32_t k, int32_t H, int64_t capacity, void* out,
+                                    int32_t* device_status, void* stream) {
   if (T < 0 || H < 1 || k < 1 || capacity < 0) return MOE_ERR_INVALID_ARG;
   if (k > 32) return MOE_ERR_UNSUPPORTED;
   if ((H % 8) != 0) return MOE_ERR_INVALID_ARG;
   if (T > (int64_t{1} << 40) || T * k >= (int64_t{1} << 30) || capacity >= (int64_t{1} << 31))
     return MOE_ERR_INVALID_ARG;
   if (T == 0) return MOE_OK;
-  if (inv_perm == nullptr || out == nullptr) return MOE_ERR_INVALID_ARG;
+  if (topk_weights == nullptr || inv_perm == nullptr || out == nullptr) return MOE_ERR_INVALID_ARG;
   if (capacity > 0 && expert_out == nullptr) return MOE_ERR_INVALID_ARG;
   if ((expert_out && !moe_host::aligned16(expert_out)) || !moe_host::aligned16(out)) return MOE_ERR_INVALID_ARG;
   CombineArgs a{};
@@ -591,17 +590,4 @@ static moe_status_t combine_rows(const void* expert_out, const float* topk_weigh
     return MOE_ERR_CUDA;
   return moe_host::launch_pdl_max_shared(kern, dim3(static_cast<unsigned>(grid)), dim3((1 + kCombineConsumerWarps) * 32), smem,
                               static_cast<cudaStream_t>(stream), a);
-}
-
-extern "C" moe_status_t moe_combine(const void* expert_out, const float* topk_weights, const int32_t* inv_perm,
-                                    int64_t T, int32_t k, int32_t H, int64_t capacity, void* out,
-                                    int32_t* device_status, void* stream) {
-  if (T > 0 && topk_weights == nullptr && k <= 32) return MOE_ERR_INVALID_ARG;
-  return combine_rows(expert_out, topk_weights, inv_perm, T, k, H, capacity, out, device_status, stream);
-}
-
-extern "C" moe_status_t moe_gather_backward(const void* grad_permuted, const int32_t* inv_perm, int64_t T, int32_t k,
-                                            int32_t H, int64_t capacity, void* grad_hidden, int32_t* device_status,
-                                            void* stream) {
-  return combine_rows(grad_permuted, nullptr, inv_perm, T, k, H, capacity, grad_hidden, device_status, stream);
 }

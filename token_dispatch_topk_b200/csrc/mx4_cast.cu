@@ -51,34 +51,63 @@ __device__ __forceinline__ uint32_t quantize8(const uint4& v, uint32_t& scale_by
   return codes;
 }
 
-// Scale byte of the lane's block, gathered over 16 lanes (four blocks, one chunk) into the chunk's word.
-__device__ __forceinline__ uint32_t chunk_word(uint32_t scale_byte, bool in_range) {
-  uint32_t b = in_range ? scale_byte : 127u;
-  b |= __shfl_down_sync(0xffffffffu, b, 4) << 8;    // lanes 0, 8 of the 16 hold blocks (0,1), (2,3)
-  b = (b & 0xffffu) | (__shfl_down_sync(0xffffffffu, b, 8) << 16);
-  return b;  // valid in lanes 0 and 16
+// Four chunks' scale bytes to words.  Half a warp holds a chunk, four lanes a block: byte u of `bytes` is the lane's
+// block's scale in chunk u.  The result, in the lanes of block b: the word (its four blocks' bytes) of chunk b.  A
+// transpose of four by four bytes, two shuffles.
+__device__ __forceinline__ uint32_t chunk_words(uint32_t bytes) {
+  const int b = (threadIdx.x >> 2) & 3;
+  uint32_t o = __shfl_xor_sync(0xffffffffu, bytes, 4);
+  bytes = (b & 1) ? __byte_perm(bytes, o, 0x3715) : __byte_perm(bytes, o, 0x6240);
+  o = __shfl_xor_sync(0xffffffffu, bytes, 8);
+  return (b & 2) ? __byte_perm(bytes, o, 0x3276) : __byte_perm(bytes, o, 0x5410);
 }
 
-// One thread per eight elements; a warp takes 256 consecutive elements (two chunks) of a row.
+// A warp takes one 128-element chunk of kRowsPerWarp consecutive rows, half a warp a row at a time: every load of the
+// eight rows is in flight before the first is used, and the rows' scale words leave as one 32-byte sector.
+constexpr int kRowsPerWarp = 8;
+
+__device__ __forceinline__ bool warp_chunk(int64_t rows, int chunks, int64_t& row0, int& chunk) {
+  const int64_t wid = (static_cast<int64_t>(blockIdx.x) * kCastThreads + threadIdx.x) >> 5;
+  const int64_t group = wid / chunks;
+  chunk = static_cast<int>(wid - group * chunks);
+  row0 = group * kRowsPerWarp;
+  return row0 < rows;
+}
+
 __global__ void __launch_bounds__(kCastThreads)
-quantize_kernel(const uint4* __restrict__ x, int64_t rows, const int32_t* __restrict__ num_rows, int nv, int segs,
+quantize_kernel(const uint4* __restrict__ x, int64_t rows, const int32_t* __restrict__ num_rows, int nv, int chunks,
                 uint32_t* __restrict__ codes, uint32_t* __restrict__ scales) {
   moe::pdl_launch_dependents();
   moe::pdl_wait();
   const int lane = threadIdx.x & 31;
-  const int64_t wid = (static_cast<int64_t>(blockIdx.x) * kCastThreads + threadIdx.x) >> 5;
-  const int64_t row = wid / segs;
-  if (row >= rows || (num_rows != nullptr && row >= num_rows[0])) return;
-  const int v = static_cast<int>(wid - row * segs) * 32 + lane;
-  const bool in = v < nv;
-  uint32_t sb;
-  const uint32_t c = quantize8(in ? moe::ld_stream(x + row * nv + v) : make_uint4(0u, 0u, 0u, 0u), sb);
-  const uint32_t word = chunk_word(sb, in);
-  if (in) codes[row * nv + v] = c;
-  if ((lane & 15) == 0 && in) scales[static_cast<int64_t>(v >> 4) * rows + row] = word;
+  int64_t row0;
+  int c;
+  const int64_t end = num_rows == nullptr || num_rows[0] > rows ? rows : num_rows[0];
+  if (!warp_chunk(rows, chunks, row0, c) || row0 >= end) return;
+  const int v = c * 16 + (lane & 15);
+  const int64_t row = row0 + (lane >> 4);
+  uint4 in[kRowsPerWarp / 2];
+#pragma unroll
+  for (int u = 0; u < kRowsPerWarp / 2; ++u) {
+    in[u] = make_uint4(0u, 0u, 0u, 0u);
+    if (v < nv && row + 2 * u < end) in[u] = moe::ld_stream(x + (row + 2 * u) * nv + v);
+  }
+  uint32_t bytes = 0u;
+#pragma unroll
+  for (int u = 0; u < kRowsPerWarp / 2; ++u) {
+    uint32_t sb;
+    const uint32_t q = quantize8(in[u], sb);
+    if (v < nv && row + 2 * u < end) codes[(row + 2 * u) * nv + v] = q;
+    bytes |= (v < nv ? sb : 127u) << (8 * u);
+  }
+  const uint32_t word = chunk_words(bytes);
+  const int64_t to = row + 2 * ((lane >> 2) & 3);  // the row whose word this lane holds
+  if ((lane & 3) == 0 && to < end) scales[static_cast<int64_t>(c) * rows + to] = word;
 }
 
 // The permute-gather: a token's row is read and quantised once and written to each of its local rows.
+// A warp takes kPieces pieces of 256 elements, all in flight together.
+constexpr int kPieces = 4;  // (chunk_words takes four)
 __global__ void __launch_bounds__(kCastThreads)
 gather_mx4_kernel(const uint4* __restrict__ x, int64_t T, int nv, int segs, int k,
                   const int32_t* __restrict__ inv_perm, int64_t capacity, uint32_t* __restrict__ codes,
@@ -97,34 +126,36 @@ gather_mx4_kernel(const uint4* __restrict__ x, int64_t T, int nv, int segs, int 
       r = -1;
     }
   }
-  unsigned local = __ballot_sync(0xffffffffu, r >= 0);
+  const unsigned local = __ballot_sync(0xffffffffu, r >= 0);
   if (local == 0u) return;  // no local slot: the row is not read
-  const int v = static_cast<int>(wid - t * segs) * 32 + lane;
-  const bool in = v < nv;
-  uint32_t sb;
-  const uint32_t c = quantize8(in ? moe::ld_stream(x + t * nv + v) : make_uint4(0u, 0u, 0u, 0u), sb);
-  const uint32_t word = chunk_word(sb, in);
-  while (local != 0u) {
-    const int64_t dst = __shfl_sync(0xffffffffu, r, __ffs(local) - 1);
-    local &= local - 1u;
-    if (in) codes[dst * nv + v] = c;
-    if ((lane & 15) == 0 && in) scales[static_cast<int64_t>(v >> 4) * capacity + dst] = word;
+  const int v0 = static_cast<int>(wid - t * segs) * (32 * kPieces) + lane;
+  uint4 in[kPieces];
+#pragma unroll
+  for (int u = 0; u < kPieces; ++u) {
+    in[u] = make_uint4(0u, 0u, 0u, 0u);
+    if (v0 + 32 * u < nv) in[u] = moe::ld_stream(x + t * nv + v0 + 32 * u);
+  }
+  uint32_t q[kPieces], bytes = 0u;
+#pragma unroll
+  for (int u = 0; u < kPieces; ++u) {
+    uint32_t sb;
+    q[u] = quantize8(in[u], sb);
+    bytes |= (v0 + 32 * u < nv ? sb : 127u) << (8 * u);
+  }
+  const uint32_t word = chunk_words(bytes);
+  const int chunk = (v0 - lane) / 16 + 2 * ((lane >> 2) & 3) + (lane >> 4);  // the chunk whose word this lane holds
+  const bool has_word = (lane & 3) == 0 && chunk * 16 < nv;
+  for (unsigned left = local; left != 0u; left &= left - 1u) {
+    const int64_t dst = __shfl_sync(0xffffffffu, r, __ffs(left) - 1);
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u)
+      if (v0 + 32 * u < nv) codes[dst * nv + v0 + 32 * u] = q[u];
+    if (has_word) scales[static_cast<int64_t>(chunk) * capacity + dst] = word;
   }
 }
 
-// Eight codes and their scale byte -> eight bf16 (exact where the value is representable).
-__global__ void __launch_bounds__(kCastThreads)
-dequantize_kernel(const uint32_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t rows, int nv,
-                  int segs, uint4* __restrict__ out) {
-  moe::pdl_launch_dependents();
-  moe::pdl_wait();
-  const int64_t wid = (static_cast<int64_t>(blockIdx.x) * kCastThreads + threadIdx.x) >> 5;
-  const int64_t row = wid / segs;
-  if (row >= rows) return;
-  const int v = static_cast<int>(wid - row * segs) * 32 + (threadIdx.x & 31);
-  if (v >= nv) return;
-  const uint32_t c = codes[row * nv + v];
-  const uint32_t byte = scales[(static_cast<int64_t>(v >> 4) * rows + row) * 4 + ((v >> 2) & 3)];
+// Eight codes and their block's scale byte -> eight bf16 (exact where the value is representable).
+__device__ __forceinline__ uint4 dequantize8(uint32_t c, uint32_t byte) {
   // 2^(byte - 127): below a byte of 1 a subnormal, 255 NaN
   const float f = byte == 255u ? __uint_as_float(0x7fc00000u)
                                : byte == 0u ? __uint_as_float(0x00400000u) : __uint_as_float(byte << 23);
@@ -146,7 +177,32 @@ dequantize_kernel(const uint32_t* __restrict__ codes, const uint8_t* __restrict_
         : "r"(h[i]));
     o[i] = moe::pack_bf16x2(lo * f, hi * f);
   }
-  moe::st_stream(out + row * nv + v, make_uint4(o[0], o[1], o[2], o[3]));
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+__global__ void __launch_bounds__(kCastThreads)
+dequantize_kernel(const uint32_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t rows, int nv,
+                  int chunks, uint4* __restrict__ out) {
+  moe::pdl_launch_dependents();
+  moe::pdl_wait();
+  const int lane = threadIdx.x & 31;
+  int64_t row0;
+  int c;
+  if (!warp_chunk(rows, chunks, row0, c)) return;
+  const int v = c * 16 + (lane & 15);
+  const int64_t row = row0 + (lane >> 4);
+  uint32_t q[kRowsPerWarp / 2], byte[kRowsPerWarp / 2];
+#pragma unroll
+  for (int u = 0; u < kRowsPerWarp / 2; ++u) {
+    q[u] = byte[u] = 0u;
+    if (v < nv && row + 2 * u < rows) {
+      q[u] = __ldcs(codes + (row + 2 * u) * nv + v);
+      byte[u] = scales[(static_cast<int64_t>(c) * rows + row + 2 * u) * 4 + ((v >> 2) & 3)];
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kRowsPerWarp / 2; ++u)
+    if (v < nv && row + 2 * u < rows) moe::st_stream(out + (row + 2 * u) * nv + v, dequantize8(q[u], byte[u]));
 }
 
 // Sizes of a matrix in the format: K in blocks of 32, and every element index below 2^47.
@@ -154,8 +210,8 @@ bool mx4_sizes_ok(int64_t rows, int32_t K) {
   return rows >= 0 && rows < (int64_t{1} << 31) && K >= 32 && (K % 32) == 0 && K <= (1 << 20);
 }
 
-bool cast_grid(int64_t rows, int segs, unsigned* grid) {
-  const int64_t blocks = (rows * segs + kCastThreads / 32 - 1) / (kCastThreads / 32);
+bool cast_grid(int64_t warps, unsigned* grid) {
+  const int64_t blocks = (warps + kCastThreads / 32 - 1) / (kCastThreads / 32);
   *grid = static_cast<unsigned>(blocks);
   return blocks <= 0x7fffffff;
 }
@@ -169,11 +225,11 @@ extern "C" moe_status_t moe_quantize_mx4(const void* x, int64_t rows, int32_t K,
   if (x == nullptr || codes == nullptr || scales == nullptr) return MOE_ERR_INVALID_ARG;
   if (!moe_host::aligned16(x) || !moe_host::aligned16(codes) || !moe_host::aligned16(scales))
     return MOE_ERR_INVALID_ARG;
-  const int nv = K / 8, segs = (nv + 31) / 32;
+  const int nv = K / 8, chunks = (K + 127) / 128;
   unsigned grid;
-  if (!cast_grid(rows, segs, &grid)) return MOE_ERR_UNSUPPORTED;
+  if (!cast_grid((rows + kRowsPerWarp - 1) / kRowsPerWarp * chunks, &grid)) return MOE_ERR_UNSUPPORTED;
   return moe_host::launch_pdl(quantize_kernel, dim3(grid), dim3(kCastThreads), 0, static_cast<cudaStream_t>(stream),
-                              static_cast<const uint4*>(x), rows, num_rows, nv, segs, static_cast<uint32_t*>(codes),
+                              static_cast<const uint4*>(x), rows, num_rows, nv, chunks, static_cast<uint32_t*>(codes),
                               static_cast<uint32_t*>(scales));
 }
 
@@ -184,12 +240,12 @@ extern "C" moe_status_t moe_dequantize_mx4(const void* codes, const void* scales
   if (out == nullptr || codes == nullptr || scales == nullptr) return MOE_ERR_INVALID_ARG;
   if (!moe_host::aligned16(out) || !moe_host::aligned16(codes) || !moe_host::aligned16(scales))
     return MOE_ERR_INVALID_ARG;
-  const int nv = K / 8, segs = (nv + 31) / 32;
+  const int nv = K / 8, chunks = (K + 127) / 128;
   unsigned grid;
-  if (!cast_grid(rows, segs, &grid)) return MOE_ERR_UNSUPPORTED;
+  if (!cast_grid((rows + kRowsPerWarp - 1) / kRowsPerWarp * chunks, &grid)) return MOE_ERR_UNSUPPORTED;
   return moe_host::launch_pdl(dequantize_kernel, dim3(grid), dim3(kCastThreads), 0,
                               static_cast<cudaStream_t>(stream), static_cast<const uint32_t*>(codes),
-                              static_cast<const uint8_t*>(scales), rows, nv, segs, static_cast<uint4*>(out));
+                              static_cast<const uint8_t*>(scales), rows, nv, chunks, static_cast<uint4*>(out));
 }
 
 extern "C" moe_status_t moe_gather_mx4(const void* hidden, int64_t T, int32_t H, int32_t k, const int32_t* inv_perm,
@@ -203,9 +259,9 @@ extern "C" moe_status_t moe_gather_mx4(const void* hidden, int64_t T, int32_t H,
   if (capacity > 0 && (codes == nullptr || scales == nullptr)) return MOE_ERR_INVALID_ARG;
   if (!moe_host::aligned16(hidden) || !moe_host::aligned16(codes) || !moe_host::aligned16(scales))
     return MOE_ERR_INVALID_ARG;
-  const int nv = H / 8, segs = (nv + 31) / 32;
+  const int nv = H / 8, segs = (nv + 32 * kPieces - 1) / (32 * kPieces);
   unsigned grid;
-  if (!cast_grid(T, segs, &grid)) return MOE_ERR_UNSUPPORTED;
+  if (!cast_grid(T * segs, &grid)) return MOE_ERR_UNSUPPORTED;
   return moe_host::launch_pdl(gather_mx4_kernel, dim3(grid), dim3(kCastThreads), 0, static_cast<cudaStream_t>(stream),
                               static_cast<const uint4*>(hidden), T, nv, segs, static_cast<int>(k), inv_perm, capacity,
                               static_cast<uint32_t*>(codes), static_cast<uint32_t*>(scales), device_status);

@@ -1,9 +1,10 @@
-// route_grads.cu -- gradients of the routing layer: of the weighted combine and of the gating.
-// (The gradient of the permute-gather is the combine with unit weights: gather_combine.cu.)
+// route_grads.cu -- gradients of the routing layer: of the weighted combine, the permute-gather and the gating.
 //
 // Combine, out[t] = sum_j w[t,j] y[r(t,j)], with grad_out = dL/dout:
 //   dL/dy[r(t,j)] = w[t,j] grad_out[t]        one rounding to bf16
 //   dL/dw[t,j]    = sum_h grad_out[t,h] y[r(t,j),h]   fp32
+// Permute-gather, permuted[r(t,j)] = hidden[t]:
+//   dL/dhidden[t] = sum_j dL/dpermuted[r(t,j)]   fp32, one rounding to bf16
 // Gating, over the selected experts i_1..i_k with incoming g_j = dL/dw_j and G = sum_j g_j w_j:
 //   softmax over all E       dL/dx_e   = p_e (g_e - G), p = softmax(x), g_e = 0 where e is not selected
 //   softmax, renormalised    dL/dx_i_j = w_j (g_j - G), 0 elsewhere (the logits are not read)
@@ -24,12 +25,6 @@ constexpr int kUnroll = 4;
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-  return v;
-}
-
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
   return v;
 }
 
@@ -116,21 +111,73 @@ __global__ void __launch_bounds__(kWarps * 32) combine_grad_kernel(CombineGradAr
   }
 }
 
+// ---------------------------------------------------------------------------------------------- gather --
+// grad_hidden[t] = the sum of the token's local rows.  A warp takes kSumVecs vectors a lane of one token's rows and
+// adds the rows kSumRows at a time, their loads in flight together.  Rows that are not there (other ranks' experts)
+// cost nothing, which the combine's ring of fixed k-row stages cannot offer.
+constexpr int kSumVecs = 2, kSumRows = 4;
+
+__global__ void __launch_bounds__(kWarps * 32)
+gather_grad_kernel(const uint4* __restrict__ gp, const int32_t* __restrict__ inv_perm, int64_t T, int k, int nv,
+                   int segs, int64_t capacity, uint4* __restrict__ gx, int32_t* status) {
+  moe::pdl_launch_dependents();
+  moe::pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t wid = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const int64_t t = wid / segs;
+  if (t >= T) return;
+  int r = -1;
+  if (lane < k) {
+    r = inv_perm[t * k + lane];
+    if (r < -1 || static_cast<int64_t>(r) >= capacity) {
+      moe::record_status(status, MOE_ERR_BAD_ROW);
+      r = -1;
+    }
+  }
+  const int v0 = static_cast<int>(wid - t * segs) * (32 * kSumVecs) + lane;
+  float acc[kSumVecs][8];
+#pragma unroll
+  for (int u = 0; u < kSumVecs; ++u)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[u][i] = 0.f;
+  unsigned left = __ballot_sync(0xffffffffu, r >= 0);
+  while (left != 0u) {
+    uint4 in[kSumRows][kSumVecs];
+#pragma unroll
+    for (int q = 0; q < kSumRows; ++q) {
+#pragma unroll
+      for (int u = 0; u < kSumVecs; ++u) in[q][u] = make_uint4(0u, 0u, 0u, 0u);
+      if (left != 0u) {  // uniform; ascending slot order
+        const int64_t row = __shfl_sync(0xffffffffu, r, __ffs(left) - 1);
+        left &= left - 1u;
+#pragma unroll
+        for (int u = 0; u < kSumVecs; ++u)
+          if (v0 + 32 * u < nv) in[q][u] = moe::ld_stream(gp + row * nv + v0 + 32 * u);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < kSumRows; ++q)  // (a row that is not there adds +0, which changes no sum)
+#pragma unroll
+      for (int u = 0; u < kSumVecs; ++u) {
+        const uint32_t x[4] = {in[q][u].x, in[q][u].y, in[q][u].z, in[q][u].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          acc[u][2 * i] += moe::bf16_lo(x[i]);
+          acc[u][2 * i + 1] += moe::bf16_hi(x[i]);
+        }
+      }
+  }
+#pragma unroll
+  for (int u = 0; u < kSumVecs; ++u)
+    if (v0 + 32 * u < nv)
+      moe::st_plain(gx + t * nv + v0 + 32 * u,
+                    make_uint4(moe::pack_bf16x2(acc[u][0], acc[u][1]), moe::pack_bf16x2(acc[u][2], acc[u][3]),
+                               moe::pack_bf16x2(acc[u][4], acc[u][5]), moe::pack_bf16x2(acc[u][6], acc[u][7])));
+}
+
 // ---------------------------------------------------------------------------------------------- gating --
 constexpr int kGateWarps = 8;
-
-template <typename T>
-__device__ __forceinline__ float to_f32(T v);
-template <>
-__device__ __forceinline__ float to_f32<float>(float v) { return v; }
-template <>
-__device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
-template <typename T>
-__device__ __forceinline__ T from_f32(float v);
-template <>
-__device__ __forceinline__ float from_f32<float>(float v) { return v; }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+constexpr int kGateFloats = 1024;  // of shared memory a warp: the rows of a batch, and the most experts
 
 struct GateGradArgs {
   const float* gw;      // [T, k] incoming
@@ -140,68 +187,206 @@ struct GateGradArgs {
   int64_t T;
   int E, k;
   int renorm, sigmoid;
+  int rows;             // rows of a warp's batch
+  int kp_log2;          // log2 of the lanes a row's slots take (k rounded up to a power of two)
+  int g_log2;           // log2 of the lanes a row's logits take (dense)
   void* gx;             // [T, E] out
   int32_t* status;
 };
 
-// One warp per row.  Lane j < k holds selected expert j; its value goes into the row's E fp32 sums in shared
-// memory, which the warp then reads in order (for the dense softmax gradient with the recomputed probabilities).
+template <typename TX, int VEC>
+struct RowVec;
+template <>
+struct RowVec<float, 4> {
+  static __device__ __forceinline__ void load(const float* p, float (&v)[4]) {
+    const float4 u = __ldcs(reinterpret_cast<const float4*>(p));
+    v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
+  }
+  static __device__ __forceinline__ void store(float* p, const float (&v)[4]) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  }
+};
+template <>
+struct RowVec<float, 1> {
+  static __device__ __forceinline__ void load(const float* p, float (&v)[1]) { v[0] = __ldcs(p); }
+  static __device__ __forceinline__ void store(float* p, const float (&v)[1]) { *p = v[0]; }
+};
+template <>
+struct RowVec<__nv_bfloat16, 8> {
+  static __device__ __forceinline__ void load(const __nv_bfloat16* p, float (&v)[8]) {
+    const uint4 u = moe::ld_stream(reinterpret_cast<const uint4*>(p));
+    v[0] = moe::bf16_lo(u.x); v[1] = moe::bf16_hi(u.x); v[2] = moe::bf16_lo(u.y); v[3] = moe::bf16_hi(u.y);
+    v[4] = moe::bf16_lo(u.z); v[5] = moe::bf16_hi(u.z); v[6] = moe::bf16_lo(u.w); v[7] = moe::bf16_hi(u.w);
+  }
+  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&v)[8]) {
+    moe::st_plain(reinterpret_cast<uint4*>(p),
+                  make_uint4(moe::pack_bf16x2(v[0], v[1]), moe::pack_bf16x2(v[2], v[3]), moe::pack_bf16x2(v[4], v[5]),
+                             moe::pack_bf16x2(v[6], v[7])));
+  }
+};
+template <>
+struct RowVec<__nv_bfloat16, 1> {
+  static __device__ __forceinline__ void load(const __nv_bfloat16* p, float (&v)[1]) { v[0] = __bfloat162float(*p); }
+  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&v)[1]) { *p = __float2bfloat16_rn(v[0]); }
+};
+
 template <typename TX>
+__device__ __forceinline__ float one_logit(const TX* p) {
+  float v[1];
+  RowVec<TX, 1>::load(p, v);
+  return v[0];
+}
+
+// A warp takes a batch of rows.  First its lanes take the rows' slots, several rows at once (their loads and the
+// scattered logits of the logistic are what the kernel waits for), and put the selected experts' values into the rows'
+// fp32 sums in shared memory; then the rows leave in order, 16 bytes a lane where E allows it (VEC), the dense softmax
+// gradient with the probabilities recomputed from CPL vectors of logits a lane, in one read.
+template <typename TX, int VEC, int CPL, bool kDense>
 __global__ void __launch_bounds__(kGateWarps * 32) gate_grad_kernel(GateGradArgs a) {
-  extern __shared__ float s_rows[];
+  __shared__ __align__(16) float s_rows[kGateWarps][kGateFloats];
+  __shared__ float s_sum[kGateWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float* row = s_rows + static_cast<size_t>(warp) * a.E;
+  float* sums = s_rows[warp];
+  const int E = a.E, k = a.k;
+  const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kGateWarps + warp) * a.rows;
+  const int n = a.T - t0 < a.rows ? static_cast<int>(a.T - t0) : a.rows;  // may be 0 or less
+  for (int i = lane * 4; i < n * E; i += 128) *reinterpret_cast<float4*>(sums + i) = make_float4(0.f, 0.f, 0.f, 0.f);
   moe::pdl_launch_dependents();
   moe::pdl_wait();
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * kGateWarps + warp;
-  if (t >= a.T) return;
-  const TX* x = static_cast<const TX*>(a.x) + t * a.E;
-  TX* gx = static_cast<TX*>(a.gx) + t * a.E;
-  for (int e = lane; e < a.E; e += 32) row[e] = 0.f;
-  int id = -1;
-  float g = 0.f, w = 0.f;
-  if (lane < a.k) {
-    id = a.ids[t * a.k + lane];
-    g = a.gw[t * a.k + lane];
-    w = a.w[t * a.k + lane];
-    if (id < 0 || id >= a.E) {
-      moe::record_status(a.status, MOE_ERR_BAD_EXPERT_ID);
-      id = -1;
-      g = w = 0.f;
+  if (n <= 0) return;  // uniform per warp
+  const TX* x = static_cast<const TX*>(a.x) + t0 * E;
+  TX* gx = static_cast<TX*>(a.gx) + t0 * E;
+  __syncwarp();
+  const int kp = 1 << a.kp_log2, j = lane & (kp - 1);
+  for (int r0 = 0; r0 < n; r0 += 32 >> a.kp_log2) {
+    const int r = r0 + (lane >> a.kp_log2);
+    int id = -1;
+    float g = 0.f, w = 0.f;
+    if (r < n && j < k) {
+      const int64_t s = (t0 + r) * k + j;
+      id = a.ids[s];
+      g = a.gw[s];
+      w = a.w[s];
+      if (id < 0 || id >= E) {
+        moe::record_status(a.status, MOE_ERR_BAD_EXPERT_ID);
+        id = -1;
+        g = w = 0.f;
+      }
     }
-  }
-  const float G = warp_sum(g * w);
-  const bool dense = !a.renorm && !a.sigmoid;
-  float v = dense ? g : a.renorm ? w * (g - G) : w * g;
-  if (a.sigmoid) {
-    const float xs = id >= 0 ? to_f32<TX>(x[id]) : 0.f;
-    // all scores underflowed to 0: the weights are the constant 1/k
-    const bool any = __any_sync(0xffffffffu, id >= 0 && expf(-xs) < INFINITY);
-    v = any ? v / (1.f + expf(xs)) : 0.f;
+    float G = g * w;
+    for (int d = kp >> 1; d > 0; d >>= 1) G += __shfl_xor_sync(0xffffffffu, G, d);
+    float v = kDense ? g : a.renorm ? w * (g - G) : w * g;
+    if (!kDense && a.sigmoid) {
+      const float xs = id >= 0 ? one_logit(x + static_cast<int64_t>(r) * E + id) : 0.f;
+      // all of a row's scores underflowed to 0: its weights are the constant 1/k
+      const unsigned some = __ballot_sync(0xffffffffu, id >= 0 && expf(-xs) < INFINITY);
+      const unsigned group = (kp == 32 ? 0xffffffffu : (1u << kp) - 1u) << (lane & ~(kp - 1));
+      v = (some & group) != 0u ? v / (1.f + expf(xs)) : 0.f;
+    }
+    const unsigned same = __match_any_sync(0xffffffffu, id >= 0 ? (r << 10) | id : -1 - lane);
+    const bool lead = id >= 0 && __ffs(same) - 1 == lane;
+    if (__any_sync(0xffffffffu, __popc(same) > 1)) {  // an expert named twice in a row: add in slot order
+      const float mine = v;
+      for (int m = 1; m < kp; ++m) {
+        const float o = __shfl_sync(0xffffffffu, mine, (lane & ~(kp - 1)) | ((j + m) & (kp - 1)));
+        if (j + m < kp && ((same >> (lane + m)) & 1u)) v += o;
+      }
+    }
+    if (lead) sums[r * E + id] = v;
+    if (kDense && j == 0 && r < n) s_sum[warp][r] = G;
   }
   __syncwarp();
-  const unsigned same = __match_any_sync(0xffffffffu, id >= 0 ? id : -1 - lane);
-  if (__any_sync(0xffffffffu, __popc(same) > 1)) {  // an expert named twice: add in slot order
-    for (int j = 0; j < a.k; ++j) {
-      const int ij = __shfl_sync(0xffffffffu, id, j);
-      const float vj = __shfl_sync(0xffffffffu, v, j);
-      if (lane == 0 && ij >= 0) row[ij] += vj;
+  if constexpr (kDense) {
+    const int G = 1 << a.g_log2, l = lane & (G - 1), chunks = E / VEC;
+    for (int r0 = 0; r0 < n; r0 += 32 >> a.g_log2) {
+      const int r = r0 + (lane >> a.g_log2);
+      float v[CPL][VEC];
+      float m = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < CPL; ++i) {
+        const int c = l + i * G;
+#pragma unroll
+        for (int q = 0; q < VEC; ++q) v[i][q] = -INFINITY;
+        if (r < n && c < chunks) RowVec<TX, VEC>::load(x + r * E + c * VEC, v[i]);
+#pragma unroll
+        for (int q = 0; q < VEC; ++q) m = fmaxf(m, v[i][q]);
+      }
+      for (int d = G >> 1; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+      float z = 0.f;
+#pragma unroll
+      for (int i = 0; i < CPL; ++i)
+#pragma unroll
+        for (int q = 0; q < VEC; ++q) {
+          v[i][q] = expf(v[i][q] - m);
+          if (r < n && l + i * G < chunks) z += v[i][q];
+        }
+      for (int d = G >> 1; d > 0; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
+      z = 1.f / z;
+      if (r < n) {
+        const float mean = s_sum[warp][r];
+#pragma unroll
+        for (int i = 0; i < CPL; ++i) {
+          const int c = l + i * G;
+          if (c < chunks) {
+#pragma unroll
+            for (int q = 0; q < VEC; ++q) v[i][q] = v[i][q] * z * (sums[r * E + c * VEC + q] - mean);
+            RowVec<TX, VEC>::store(gx + r * E + c * VEC, v[i]);
+          }
+        }
+      }
     }
-  } else if (id >= 0) {
-    row[id] = v;
-  }
-  __syncwarp();
-  if (dense) {
-    float m = -INFINITY;
-    for (int e = lane; e < a.E; e += 32) m = fmaxf(m, to_f32<TX>(x[e]));
-    m = warp_max(m);
-    float z = 0.f;
-    for (int e = lane; e < a.E; e += 32) z += expf(to_f32<TX>(x[e]) - m);
-    z = 1.f / warp_sum(z);
-    for (int e = lane; e < a.E; e += 32) gx[e] = from_f32<TX>(expf(to_f32<TX>(x[e]) - m) * z * (row[e] - G));
   } else {
-    for (int e = lane; e < a.E; e += 32) gx[e] = from_f32<TX>(row[e]);
+    for (int i = lane * VEC; i < n * E; i += 32 * VEC) {
+      float v[VEC];
+#pragma unroll
+      for (int q = 0; q < VEC; ++q) v[q] = sums[i + q];
+      RowVec<TX, VEC>::store(gx + i, v);
+    }
   }
+}
+
+using GateKernel = void (*)(GateGradArgs);
+
+// Vectors a lane for the dense gradient: the next of {1, 2, 4} (16-byte vectors of bf16), {1, 2, 8} (of fp32) or
+// {2, 8, 32} (single elements) that holds E experts.
+template <typename TX, int VEC>
+GateKernel dense_kernel(int cpl) {
+  if constexpr (VEC == 8) {
+    return cpl <= 1 ? gate_grad_kernel<TX, 8, 1, true>
+                    : cpl <= 2 ? gate_grad_kernel<TX, 8, 2, true> : gate_grad_kernel<TX, 8, 4, true>;
+  } else if constexpr (VEC == 4) {
+    return cpl <= 1 ? gate_grad_kernel<TX, 4, 1, true>
+                    : cpl <= 2 ? gate_grad_kernel<TX, 4, 2, true> : gate_grad_kernel<TX, 4, 8, true>;
+  } else {
+    return cpl <= 2 ? gate_grad_kernel<TX, 1, 2, true>
+                    : cpl <= 8 ? gate_grad_kernel<TX, 1, 8, true> : gate_grad_kernel<TX, 1, 32, true>;
+  }
+}
+
+template <typename TX>
+moe_status_t launch_gate_grad(GateGradArgs a, cudaStream_t st) {
+  constexpr int kWide = 16 / sizeof(TX);
+  const bool dense = !a.renorm && !a.sigmoid;
+  const bool wide = a.E % kWide == 0 && moe_host::aligned16(a.gx) && (!dense || moe_host::aligned16(a.x));
+  const int chunks = wide ? a.E / kWide : a.E;
+  a.kp_log2 = 0;
+  while ((1 << a.kp_log2) < a.k) ++a.kp_log2;
+  a.g_log2 = 0;
+  while ((1 << a.g_log2) < chunks && a.g_log2 < 5) ++a.g_log2;
+  const int cpl = (chunks + 31) / 32;
+  // rows of a batch: as many as fit a warp's shared memory, fewer where that would leave the SMs fewer than 16 warps
+  const int sms = moe_host::sm_count();
+  if (sms <= 0) return MOE_ERR_CUDA;
+  a.rows = 1;
+  while (a.rows < 32 && 2 * a.rows * a.E <= kGateFloats && a.T >= int64_t{2} * a.rows * sms * 16) a.rows *= 2;
+  GateKernel kernel;
+  if (wide)
+    kernel = dense ? dense_kernel<TX, kWide>(cpl) : static_cast<GateKernel>(gate_grad_kernel<TX, kWide, 1, false>);
+  else
+    kernel = dense ? dense_kernel<TX, 1>(cpl) : static_cast<GateKernel>(gate_grad_kernel<TX, 1, 1, false>);
+  const int64_t batches = (a.T + a.rows - 1) / a.rows;
+  return moe_host::launch_pdl(kernel, dim3(static_cast<unsigned>((batches + kGateWarps - 1) / kGateWarps)),
+                              dim3(kGateWarps * 32), 0, st, a);
 }
 
 }  // namespace
@@ -275,9 +460,27 @@ extern "C" moe_status_t moe_topk_softmax_backward(const float* grad_topk_weights
   a.k = k;
   a.gx = grad_logits;
   a.status = device_status;
-  const int64_t grid = (T + kGateWarps - 1) / kGateWarps;
-  const size_t smem = static_cast<size_t>(kGateWarps) * E * sizeof(float);  // <= 32 KB
-  return moe_host::launch_pdl(dtype == MOE_DTYPE_BF16 ? gate_grad_kernel<__nv_bfloat16> : gate_grad_kernel<float>,
-                              dim3(static_cast<unsigned>(grid)), dim3(kGateWarps * 32), smem,
-                              static_cast<cudaStream_t>(stream), a);
+  return dtype == MOE_DTYPE_BF16 ? launch_gate_grad<__nv_bfloat16>(a, static_cast<cudaStream_t>(stream))
+                                 : launch_gate_grad<float>(a, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" moe_status_t moe_gather_backward(const void* grad_permuted, const int32_t* inv_perm, int64_t T, int32_t k,
+                                            int32_t H, int64_t capacity, void* grad_hidden, int32_t* device_status,
+                                            void* stream) {
+  if (T < 0 || H < 1 || k < 1 || capacity < 0) return MOE_ERR_INVALID_ARG;
+  if (k > 32) return MOE_ERR_UNSUPPORTED;
+  if ((H % 8) != 0) return MOE_ERR_INVALID_ARG;
+  if (T > (int64_t{1} << 40) || T * k >= (int64_t{1} << 30) || capacity >= (int64_t{1} << 31))
+    return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (inv_perm == nullptr || grad_hidden == nullptr || (capacity > 0 && grad_permuted == nullptr))
+    return MOE_ERR_INVALID_ARG;
+  if (!moe_host::aligned16(grad_permuted) || !moe_host::aligned16(grad_hidden)) return MOE_ERR_INVALID_ARG;
+  const int nv = H / 8, segs = (nv + 32 * kSumVecs - 1) / (32 * kSumVecs);
+  const int64_t grid = (T * segs + kWarps - 1) / kWarps;
+  if (grid > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
+  return moe_host::launch_pdl(gather_grad_kernel, dim3(static_cast<unsigned>(grid)), dim3(kWarps * 32), 0,
+                              static_cast<cudaStream_t>(stream), static_cast<const uint4*>(grad_permuted), inv_perm, T,
+                              static_cast<int>(k), nv, segs, capacity, static_cast<uint4*>(grad_hidden),
+                              device_status);
 }
