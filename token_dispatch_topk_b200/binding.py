@@ -376,57 +376,58 @@ def moe_read_status(device_status_word: torch.Tensor, stream=None) -> int:
 
 
 # ------------------------------------------------------------ gradients and 4-bit products --
-def _arg(t, name: str, dtype, shape, device: torch.device, optional: bool = False):
-    """Pointer of a contiguous CUDA tensor of this dtype, shape and device (ValueError otherwise); None stays None."""
+# A decode-sized kernel runs in a few microseconds, so what these wrappers do before the launch counts: one test of a
+# good tensor, reasons only for a bad one; the raw current stream (0.1 us) instead of a Stream object (3 us).
+def _arg(t, name: str, dtype, shape, index: int) -> int:
+    """Address of a contiguous CUDA tensor of this dtype and shape on device `index` (ValueError otherwise)."""
+    if t is not None and t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+        return t.data_ptr()
     if t is None:
-        if optional:
-            return None
         raise ValueError(f"{name} is missing")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (the routing path runs only on the GPU)")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
-    if t.dtype != dtype:
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the other tensors on cuda:{index}")
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _matrix(t, name: str, dtype=None):
-    if t is None or t.dim() != 2 or (dtype is not None and t.dtype != dtype):
-        raise ValueError(f"{name} must be a matrix" + (f" of {dtype}" if dtype is not None else ""))
+def _matrix(t, name: str):
+    if t is None or t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix")
     return t.shape
 
 
-def _call(name: str, device: torch.device, stream, *args) -> None:
-    """Run an entry point with `device` current, on `stream` or that device's current stream (the last argument)."""
-    if device.type != "cuda":
+def _call(name: str, index: int, stream, *args) -> None:
+    """Run an entry point with device `index` current, on `stream` or that device's current stream (the last argument)."""
+    if index < 0:
         raise ValueError(f"{name} needs CUDA tensors (the routing path runs only on the GPU)")
-    if isinstance(stream, torch.cuda.Stream) and stream.device != device:
-        raise ValueError(f"{name}: the stream belongs to {stream.device}, the tensors to {device}")
-    fn = getattr(load_library(), name)
-    if torch.cuda.current_device() == device.index:
-        st = fn(*args, _stream(stream))
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(index)
+    elif isinstance(stream, torch.cuda.Stream):
+        if stream.device.index != index:
+            raise ValueError(f"{name}: the stream belongs to {stream.device}, the tensors to cuda:{index}")
+        stream = stream.cuda_stream
+    fn = getattr(_lib or load_library(), name)
+    if torch.cuda.current_device() == index:
+        st = fn(*args, stream)
     else:
-        with torch.cuda.device(device):
-            st = fn(*args, _stream(stream))
-    _check(st, name)
+        with torch.cuda.device(index):
+            st = fn(*args, stream)
+    if st != MOE_OK:
+        raise MoeError(st, name)
 
 
-def _slots(inv_perm, T: int, k: int, device) -> int:
-    return _arg(inv_perm, "inv_perm", torch.int32, (T * k,), device)
-
-
-def _status_arg(device_status, device):
-    """The status word: the first element of an int32 tensor (a workspace, or a word of its own)."""
+def _status_arg(device_status, index: int):
+    """The status word: the first element of an int32 tensor (a workspace, or a word of its own), or None."""
     if device_status is None:
         return None
     if device_status.numel() < 1:
         raise ValueError("device_status must hold a word")
-    return _arg(device_status, "device_status", torch.int32, tuple(device_status.shape), device)
+    return _arg(device_status, "device_status", torch.int32, device_status.shape, index)
 
 
 def moe_combine_backward(grad_out: torch.Tensor, expert_out: torch.Tensor, topk_weights: torch.Tensor,
@@ -443,19 +444,20 @@ def moe_combine_backward(grad_out: torch.Tensor, expert_out: torch.Tensor, topk_
     T, H = _matrix(grad_out, "grad_out")
     k = _matrix(topk_weights, "topk_weights")[1]
     capacity = _matrix(expert_out, "expert_out")[0]
-    dev, bf16 = grad_out.device, torch.bfloat16
+    dev, bf16 = grad_out.get_device(), torch.bfloat16
     if grad_expert_out is None:
-        grad_expert_out = torch.empty((capacity, H), dtype=bf16, device=dev)
+        grad_expert_out = torch.empty((capacity, H), dtype=bf16, device=grad_out.device)
     if grad_topk_weights is None:
-        grad_topk_weights = torch.empty((T, k), dtype=torch.float32, device=dev)
+        grad_topk_weights = torch.empty((T, k), dtype=torch.float32, device=grad_out.device)
     pads = (None, None)
     if zero_pad:
         pads = (_arg(sorted_token_ids, "sorted_token_ids", torch.int32, (capacity,), dev),
                 _arg(num_tokens_post_pad, "num_tokens_post_pad", torch.int32, (1,), dev))
     _call("moe_combine_backward", dev, stream, _arg(grad_out, "grad_out", bf16, (T, H), dev),
           _arg(expert_out, "expert_out", bf16, (capacity, H), dev),
-          _arg(topk_weights, "topk_weights", torch.float32, (T, k), dev), _slots(inv_perm, T, k, dev), *pads, T, k, H,
-          capacity, MOE_GATHER_ZERO_PAD if zero_pad else 0,
+          _arg(topk_weights, "topk_weights", torch.float32, (T, k), dev),
+          _arg(inv_perm, "inv_perm", torch.int32, (T * k,), dev), *pads, T, k, H, capacity,
+          MOE_GATHER_ZERO_PAD if zero_pad else 0,
           _arg(grad_expert_out, "grad_expert_out", bf16, (capacity, H), dev),
           _arg(grad_topk_weights, "grad_topk_weights", torch.float32, (T, k), dev), _status_arg(device_status, dev))
     return grad_expert_out, grad_topk_weights
@@ -469,12 +471,12 @@ def moe_gather_backward(grad_permuted: torch.Tensor, inv_perm: torch.Tensor, k: 
     capacity, H = _matrix(grad_permuted, "grad_permuted")
     if k < 1 or inv_perm.numel() % k != 0:
         raise ValueError(f"inv_perm must hold T * k slots, got {inv_perm.numel()} with k = {k}")
-    T, dev = inv_perm.numel() // k, grad_permuted.device
+    T, dev = inv_perm.numel() // k, grad_permuted.get_device()
     if grad_hidden is None:
-        grad_hidden = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+        grad_hidden = torch.empty((T, H), dtype=torch.bfloat16, device=grad_permuted.device)
     _call("moe_gather_backward", dev, stream,
-          _arg(grad_permuted, "grad_permuted", torch.bfloat16, (capacity, H), dev), _slots(inv_perm, T, k, dev), T, k, H,
-          capacity, _arg(grad_hidden, "grad_hidden", torch.bfloat16, (T, H), dev), _status_arg(device_status, dev))
+          _arg(grad_permuted, "grad_permuted", torch.bfloat16, (capacity, H), dev),
+          _arg(inv_perm, "inv_perm", torch.int32, (T * k,), dev), T, k, H, capacity, _arg(grad_hidden, "grad_hidden", torch.bfloat16, (T, H), dev), _status_arg(device_status, dev))
     return grad_hidden
 
 
@@ -486,11 +488,11 @@ def moe_topk_softmax_backward(grad_topk_weights: torch.Tensor, logits: torch.Ten
     topk_weights and topk_ids are what moe_topk_softmax returned with the same renormalize and scoring."""
     T, E = _matrix(logits, "logits")
     k = _matrix(topk_weights, "topk_weights")[1]
-    dev, dtype = logits.device, logits.dtype
+    dev, dtype = logits.get_device(), logits.dtype
     if dtype not in (torch.bfloat16, torch.float32):
         raise ValueError(f"logits dtype {dtype} unsupported (bf16 or fp32)")
     if grad_logits is None:
-        grad_logits = torch.empty((T, E), dtype=dtype, device=dev)
+        grad_logits = torch.empty((T, E), dtype=dtype, device=logits.device)
     f32 = torch.float32
     _call("moe_topk_softmax_backward", dev, stream, _arg(grad_topk_weights, "grad_topk_weights", f32, (T, k), dev),
           _arg(logits, "logits", dtype, (T, E), dev), MOE_DTYPE_BF16 if dtype == torch.bfloat16 else MOE_DTYPE_F32,
@@ -521,10 +523,10 @@ def alloc_mx4(rows: int, K: int, device) -> Mx4Tensor:
                      torch.empty((-(-K // 128), rows, 4), dtype=torch.uint8, device=device))
 
 
-def _mx4_args(q: Mx4Tensor, name: str, device):
-    _matrix(q.codes, f"{name}.codes")
-    return (_arg(q.codes, f"{name}.codes", torch.uint8, (q.rows, q.K // 2), device),
-            _arg(q.scales, f"{name}.scales", torch.uint8, (-(-q.K // 128), q.rows, 4), device))
+def _mx4_args(q: Mx4Tensor, codes_name: str, scales_name: str, index: int):
+    rows, half = _matrix(q.codes, codes_name)
+    return (_arg(q.codes, codes_name, torch.uint8, (rows, half), index),
+            _arg(q.scales, scales_name, torch.uint8, ((half + 63) // 64, rows, 4), index))
 
 
 def _mx4_out(out: Optional[Mx4Tensor], rows: int, K: int, device) -> Mx4Tensor:
@@ -541,19 +543,20 @@ def moe_quantize_mx4(x: torch.Tensor, out: Optional[Mx4Tensor] = None, num_rows:
     rows from there on are neither read nor written."""
     rows, K = _matrix(x, "x")
     out = _mx4_out(out, rows, K, x.device)
-    _call("moe_quantize_mx4", x.device, stream, _arg(x, "x", torch.bfloat16, (rows, K), x.device), rows, K,
-          _arg(num_rows, "num_rows", torch.int32, (1,), x.device, optional=True),
-          *_mx4_args(out, "out", x.device))
+    dev = x.get_device()
+    _call("moe_quantize_mx4", dev, stream, _arg(x, "x", torch.bfloat16, (rows, K), dev), rows, K,
+          None if num_rows is None else _arg(num_rows, "num_rows", torch.int32, (1,), dev),
+          *_mx4_args(out, "out.codes", "out.scales", dev))
     return out
 
 
 def moe_dequantize_mx4(q: Mx4Tensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The values of q as bf16 [rows, K]."""
-    dev = q.codes.device
+    dev, rows, K = q.codes.get_device(), q.rows, q.K
     if out is None:
-        out = torch.empty((q.rows, q.K), dtype=torch.bfloat16, device=dev)
-    _call("moe_dequantize_mx4", dev, stream, *_mx4_args(q, "q", dev), q.rows, q.K,
-          _arg(out, "out", torch.bfloat16, (q.rows, q.K), dev))
+        out = torch.empty((rows, K), dtype=torch.bfloat16, device=q.codes.device)
+    _call("moe_dequantize_mx4", dev, stream, *_mx4_args(q, "q.codes", "q.scales", dev), rows, K,
+          _arg(out, "out", torch.bfloat16, (rows, K), dev))
     return out
 
 
@@ -563,10 +566,11 @@ def moe_gather_mx4(hidden: torch.Tensor, k: int, inv_perm: torch.Tensor, capacit
     """moe_gather in microscaled 4-bit floating point: hidden [T, H] bf16 -> expert-grouped rows [capacity, H].
     Rows of no slot are left as they were."""
     T, H = _matrix(hidden, "hidden")
-    dev = hidden.device
-    out = _mx4_out(out, capacity, H, dev)
+    dev = hidden.get_device()
+    out = _mx4_out(out, capacity, H, hidden.device)
     _call("moe_gather_mx4", dev, stream, _arg(hidden, "hidden", torch.bfloat16, (T, H), dev), T, H, k,
-          _slots(inv_perm, T, k, dev), capacity, *_mx4_args(out, "out", dev), _status_arg(device_status, dev))
+          _arg(inv_perm, "inv_perm", torch.int32, (T * k,), dev), capacity,
+          *_mx4_args(out, "out.codes", "out.scales", dev), _status_arg(device_status, dev))
     return out
 
 
@@ -576,19 +580,20 @@ def moe_grouped_gemm_mx4(x: Mx4Tensor, w: Mx4Tensor, counts: torch.Tensor, offse
     """The experts' product on expert-grouped rows: x [capacity, K], w [E_local * N, K] (expert e's feature n in row
     e * N + n), counts [E_local] and offsets [E_local + 1] as from moe_align_permute -> out [capacity, N] bf16, or
     [capacity, N/2] = silu(first half) * second half with swiglu.  Rows of no expert are left as they were."""
-    dev = x.codes.device
-    E, capacity, K = counts.numel(), x.rows, x.K
-    if E < 1 or w.rows % E != 0:
-        raise ValueError(f"w must hold E_local * N rows, got {w.rows} for {E} experts")
+    dev = x.codes.get_device()
+    E, capacity, K, w_rows = counts.numel(), x.rows, x.K, w.rows
+    if E < 1 or w_rows % E != 0:
+        raise ValueError(f"w must hold E_local * N rows, got {w_rows} for {E} experts")
     if w.K != K:
         raise ValueError(f"x has rows of {K}, w of {w.K}")
-    N = w.rows // E
+    N = w_rows // E
     if swiglu and N % 2 != 0:
         raise ValueError(f"swiglu needs an even number of features, got {N}")
     cols = N // 2 if swiglu else N
     if out is None:
-        out = torch.empty((capacity, cols), dtype=torch.bfloat16, device=dev)
-    _call("moe_grouped_gemm_mx4", dev, stream, *_mx4_args(x, "x", dev), *_mx4_args(w, "w", dev),
+        out = torch.empty((capacity, cols), dtype=torch.bfloat16, device=x.codes.device)
+    _call("moe_grouped_gemm_mx4", dev, stream, *_mx4_args(x, "x.codes", "x.scales", dev),
+          *_mx4_args(w, "w.codes", "w.scales", dev),
           _arg(counts, "counts", torch.int32, (E,), dev), _arg(offsets, "offsets", torch.int32, (E + 1,), dev), E,
           capacity, N, K, MOE_MX4_SWIGLU if swiglu else 0, _arg(out, "out", torch.bfloat16, (capacity, cols), dev),
           _status_arg(device_status, dev))

@@ -45,22 +45,24 @@ struct CombineGradArgs {
   int32_t* status;
 };
 
-constexpr int kPadRowsPerCta = 256;
+constexpr int kPadRowsPerCta = kWarps * 32;
 
 // One warp per slot; the k slots of a token sit in neighbouring warps, so its gradient row comes from DRAM once
 // and from L1 / L2 after that.  Bandwidth-bound: a row of y in, a row of gy out, 16 bytes a lane and kUnroll
 // vectors in flight.
 __global__ void __launch_bounds__(kWarps * 32) combine_grad_kernel(CombineGradArgs a) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   moe::pdl_launch_dependents();
   moe::pdl_wait();  // every input may come from the previous kernel
   if (blockIdx.x >= a.slot_blocks) {  // +0 into the pad rows below N_pad (their sorted id is T*k)
     const int64_t p0 = (static_cast<int64_t>(blockIdx.x) - a.slot_blocks) * kPadRowsPerCta;
     int64_t end = a.n_pad[0];
     if (end > a.capacity) end = a.capacity;
-    for (int64_t p = p0 + warp; p < p0 + kPadRowsPerCta && p < end; p += kWarps) {
-      if (a.sorted_ids[p] != static_cast<int32_t>(a.slots)) continue;
-      for (int v = lane; v < a.nv; v += 32) moe::st_plain(a.gy + p * a.nv + v, make_uint4(0u, 0u, 0u, 0u));
+    const int64_t p = p0 + tid;  // a lane looks at a row, the warp then writes its pad rows one by one
+    unsigned pads = __ballot_sync(0xffffffffu, p < end && a.sorted_ids[p] == static_cast<int32_t>(a.slots));
+    for (; pads != 0u; pads &= pads - 1u) {
+      uint4* row = a.gy + (p0 + warp * 32 + __ffs(pads) - 1) * a.nv;
+      for (int v = lane; v < a.nv; v += 32) moe::st_plain(row + v, make_uint4(0u, 0u, 0u, 0u));
     }
     return;
   }
