@@ -11,7 +11,7 @@
 // gate and the 16 matching up features, so that one thread holds both.  The rows of an expert are split evenly over as
 // few tiles as hold them.
 //
-// Two forms (Shape<1>, Shape<2>): for few rows an expert, one CTA a tile, 128 features by up to 64 rows, a deep ring of
+// Two forms (Shape): for few rows an expert, one CTA a tile, 128 features by up to 64 rows, a deep ring of
 // stages; for many, a pair of CTAs a tile (cta_group::2), 256 features by up to 224 rows, each CTA loading its own
 // 128 features and half of the rows, which halves what comes through L2 per product.
 //
@@ -37,15 +37,15 @@ constexpr int kBoxRows = 16;            // rows of the smallest TMA box of x; ga
 constexpr int kBytesA = kTileF * kStageK / 2;
 constexpr int kAtom = 512;              // scales of 128 rows by 128 elements
 constexpr int kEpiT = 32;               // columns an epilogue warp takes at a time
-constexpr int kEpiBytes = kEpiT * 64;   // its transposed block: rows of 32 (with the gate 16) bf16, swizzled
 constexpr int kMaxExperts = 1024;
 constexpr uint32_t kTmemCols = 512;
 
-template <int CG>  // CTAs a tile
+template <int CG, bool kGate>  // CTAs a tile; whether silu(gate) * up follows
 struct Shape {
   static constexpr int kTileT = CG == 1 ? 64 : 224;  // rows a tile, at most
   static constexpr int kStepT = CG == 1 ? 16 : 32;   // columns of a product: a multiple of this
-  static constexpr int kStages = CG == 1 ? 7 : 5;
+  static constexpr int kStages = CG == 1 ? 7 : kGate ? 6 : 5;  // (as shared memory allows)
+  static constexpr int kEpiBytes = kEpiT * (kGate ? 32 : 64);  // an epilogue warp's transposed block
   static constexpr int kRowsB = kTileT / CG;         // rows of x a CTA loads
   static constexpr int kBytesB = kRowsB * kStageK / 2;
   static constexpr int kStageBytes = kBytesA + kBytesB;
@@ -79,7 +79,6 @@ struct ProductArgs {
   int chunks;     // ceil(K / 128)
   int kstages;    // ceil(K / 256)
   int ftiles;     // feature tiles (of a CTA, or of a pair)
-  int gate;       // 1: silu(gate) * up
   int gate_box;   // 1: map_w has the gate's boxes (N a multiple of 32), 0: boxes of 16 rows
   int64_t capacity;
   __nv_bfloat16* out;
@@ -179,6 +178,19 @@ __device__ __forceinline__ bool phase_done(uint64_t* bar, uint32_t parity) {
       : "memory");
   return done != 0u;
 }
+__device__ __forceinline__ bool phases_done(uint64_t* bar, uint32_t parity, uint64_t* bar2, uint32_t parity2) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
+      "and.pred p, p, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(moe::smem_addr(bar)), "r"(parity), "r"(moe::smem_addr(bar2)), "r"(parity2)
+      : "memory");
+  return done != 0u;
+}
 __device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
@@ -230,14 +242,6 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, wait_slow(bar, parity, abort, status));
 }
 
-// Two of them, their first tests in flight together.
-__device__ __forceinline__ bool wait_both(uint64_t* bar, uint32_t parity, uint64_t* bar2, uint32_t parity2,
-                                          volatile int* abort, int32_t* status) {
-  const bool one = phase_done(bar, parity), two = bar2 == nullptr || phase_done(bar2, parity2);
-  if (__all_sync(0xffffffffu, one && two)) return true;
-  return wait_warp(bar, parity, abort, status) && (bar2 == nullptr || wait_warp(bar2, parity2, abort, status));
-}
-
 // One lane of a converged warp, always the same.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -247,7 +251,7 @@ __device__ __forceinline__ bool elect_one() {
 
 // Tile t: its first row, and 10 bits of expert, 8 of rows, 13 of feature tile.  (By value, not a method: a struct whose
 // address is taken lives in local memory.)
-template <int CG>
+template <int kTileStep>
 __device__ __noinline__ int2 tile_of(int t, const int32_t* first, const int32_t* counts, const int32_t* offsets, int E,
                                      int ftiles) {
   const int rt = t / ftiles, ft = t - rt * ftiles;
@@ -258,15 +262,15 @@ __device__ __noinline__ int2 tile_of(int t, const int32_t* first, const int32_t*
     else hi = mid - 1;
   }
   const int cnt = counts[lo], n = first[lo + 1] - first[lo], i = rt - first[lo];
-  constexpr int kStep = Shape<CG>::kStepT;
-  const int per = ((cnt + n - 1) / n + kStep - 1) / kStep * kStep;  // at most kTileT
+  const int per = ((cnt + n - 1) / n + kTileStep - 1) / kTileStep * kTileStep;  // at most kTileT
   return make_int2(offsets[lo] + i * per, (lo << 21) | ((cnt - i * per < per ? cnt - i * per : per) << 13) | ft);
 }
 
 // The tiles of this CTA (or pair), in order: expert by expert, then row tiles, features fastest.  The lanes of a warp
 // work out 32 tiles at a time (a search, a division and two loads each, over 1000 cycles), which next() passes round.
-template <int CG>
+template <int CG, bool kGate>
 struct Tiles {
+  static constexpr int kStep = Shape<CG, kGate>::kStepT;
   const ProductArgs& a;
   const int32_t* first;  // row tiles before expert e
   int e, f, row0, rows;  // expert, this CTA's feature tile, the tile's first row, its rows
@@ -281,7 +285,7 @@ struct Tiles {
     if (turn == 32) {
       const int t = at + static_cast<int>(threadIdx.x & 31) * static_cast<int>(gridDim.x / CG);
       mine = make_int2(0, 0);
-      if (t < total) mine = tile_of<CG>(t, first, a.counts, a.offsets, a.E, a.ftiles);
+      if (t < total) mine = tile_of<kStep>(t, first, a.counts, a.offsets, a.E, a.ftiles);
       __syncwarp();
       turn = 0;
     }
@@ -295,26 +299,26 @@ struct Tiles {
     return true;
   }
   // the product's columns
-  __device__ __forceinline__ int cols() const { return (rows + Shape<CG>::kStepT - 1) / Shape<CG>::kStepT * Shape<CG>::kStepT; }
+  __device__ __forceinline__ int cols() const { return (rows + kStep - 1) / kStep * kStep; }
   // the first weight row of the tile (with the gate: of its gate features)
   __device__ __forceinline__ int64_t weight_row0() const {
-    return static_cast<int64_t>(e) * a.N + static_cast<int64_t>(f) * (a.gate ? kTileF / 2 : kTileF);
+    return static_cast<int64_t>(e) * a.N + static_cast<int64_t>(f) * (kGate ? kTileF / 2 : kTileF);
   }
   // row of the weights that lane m of the tile holds (clamped: lanes past the expert's features are not stored)
   __device__ __forceinline__ int64_t weight_row(int m) const {
-    const int64_t r = weight_row0() + (!a.gate ? m : (m & 16 ? a.N / 2 : 0) + (m >> 5) * 16 + (m & 15));
+    const int64_t r = weight_row0() + (!kGate ? m : (m & 16 ? a.N / 2 : 0) + (m >> 5) * 16 + (m & 15));
     const int64_t last = static_cast<int64_t>(a.E) * a.N - 1;
     return r < last ? r : last;
   }
 };
 
-template <int CG>
+template <int CG, bool kGate>
 __global__ void __launch_bounds__(kThreads, 1)
 grouped_mx4_kernel(const __grid_constant__ CUtensorMap map_x16, const __grid_constant__ CUtensorMap map_x32,
                    const __grid_constant__ CUtensorMap map_x64, const __grid_constant__ CUtensorMap map_x,
                    const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_out,
                    const ProductArgs a) {
-  using S = Shape<CG>;
+  using S = Shape<CG, kGate>;
   constexpr int kStages = S::kStages;
   extern __shared__ uint8_t smem_raw[];
   typename S::Smem& s =
@@ -397,7 +401,7 @@ grouped_mx4_kernel(const __grid_constant__ CUtensorMap map_x16, const __grid_con
   volatile int* abort = &s.abort;
 
   if (warp == 0) {
-    Tiles<CG> tl(a, s.first_tile);
+    Tiles<CG, kGate> tl(a, s.first_tile);
     int st = 0;
     uint32_t round = 0;
     int64_t issued = 0;
@@ -418,7 +422,7 @@ grouped_mx4_kernel(const __grid_constant__ CUtensorMap map_x16, const __grid_con
           moe::mbar_arrive_expect_tx(&s.full[st], kBytesA + box * 128);
           const int x = kb * 128;
           uint8_t* dst = s.ab[st];
-          if (!a.gate) {
+          if (!kGate) {
             tma_load_2d(dst, &map_w, x, wr, &s.full[st]);
           } else if (a.gate_box) {
             tma_load_gate(dst, &map_w, x, tl.f * (kTileF / 2 / kBoxRows), tl.e, &s.full[st]);
@@ -443,13 +447,11 @@ grouped_mx4_kernel(const __grid_constant__ CUtensorMap map_x16, const __grid_con
   } else if (warp == 1 && rank == 0) {
     // instruction descriptor: A and B e2m1, scales e8m0, 128 lanes a CTA; columns and scale ids below
     constexpr uint32_t kDesc = (1u << 7) | (1u << 10) | (1u << 23) | ((CG * 128u >> 4) << 24);
-    Tiles<CG> tl(a, s.first_tile);
+    Tiles<CG, kGate> tl(a, s.first_tile);
     const uint64_t da0 = desc_sw128(moe::smem_addr(s.ab[0])), sf0 = desc_plain(moe::smem_addr(s.sf[0]));
-    int st = 0;
-    uint32_t round = 0, buf = 0, buf_round = 0, set = 0;
-    int st2 = 0;  // the stage two before this one, and its round
-    uint32_t round2 = 0;
-    int before = 0;  // stages before this one, up to 2
+    int st = 0, st2 = 0;  // the stage, and the one two before it
+    uint32_t round = 0, round2 = 0, buf = 0, buf_round = 0, set = 0;
+    int before = 0;      // stages before this one, up to 2
     bool ok = true;
     while (ok && tl.next()) {
       if (!wait_warp(&s.acc_empty[buf], (buf_round & 1u) ^ 1u, abort, a.status)) break;
@@ -458,35 +460,40 @@ grouped_mx4_kernel(const __grid_constant__ CUtensorMap map_x16, const __grid_con
       const uint32_t d = tmem + buf * S::kTileT;
       for (int kb = 0; kb < a.kstages; ++kb) {
         // the stage is there, and the products that read this set of TMEM scales, two stages ago, are done
-        if (!wait_both(&s.full[st], round & 1u, before < 2 ? nullptr : &s.empty[st2], round2 & 1u, abort, a.status)) {
-          ok = false;
-          break;
+        // (one test of both: a test takes about 100 cycles to answer)
+        const bool older = before == 2;
+        if (!__all_sync(0xffffffffu, phases_done(&s.full[st], round & 1u, older ? &s.empty[st2] : &s.full[st],
+                                                 (older ? round2 : round) & 1u))) {
+          ok = wait_warp(&s.full[st], round & 1u, abort, a.status) &&
+               (!older || wait_warp(&s.empty[st2], round2 & 1u, abort, a.status));
+          if (!ok) break;
         }
-        if (before == 2) {
+        if (older) {
           if (++st2 == kStages) { st2 = 0; ++round2; }
         } else {
           ++before;
         }
+        const int now = st;
+        if (++st == kStages) { st = 0; ++round; }
         moe::fence_proxy_async_smem();  // the scales were written by ordinary copies
         tmem_fence_after();
         if (elect_one()) {
           const uint32_t sf = tmem + S::kTmemSf + set * S::kSfCols;
-          const uint64_t sfd = sf0 + static_cast<uint32_t>(st * (S::kBytesSf >> 4));
+          const uint64_t sfd = sf0 + static_cast<uint32_t>(now * (S::kBytesSf >> 4));
 #pragma unroll
           for (int i = 0; i < S::kBytesSf / kAtom; ++i) sf_to_tmem<CG>(sf + 4 * i, sfd + i * (kAtom >> 4));
-          const uint64_t da = da0 + static_cast<uint32_t>(st * (S::kStageBytes >> 4)), db = da + (kBytesA >> 4);
+          const uint64_t da = da0 + static_cast<uint32_t>(now * (S::kStageBytes >> 4)), db = da + (kBytesA >> 4);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {  // 64 elements: 32 bytes further in the swizzle atom
             const uint32_t id = (kk & 1) * 2;  // which two of the chunk's four scales
             mma_mx4<CG>(d, da + kk * 2, db + kk * 2, idesc | (id << 4) | (id << 29), sf + 4 * (kk >> 1),
                         sf + 8 + 4 * S::kAtomsB * (kk >> 1), kb > 0 || kk > 0);
           }
-          commit<CG>(&s.empty[st]);
+          commit<CG>(&s.empty[now]);
           if (kb == a.kstages - 1) commit<CG>(&s.acc_full[buf]);
         }
         __syncwarp();
         set ^= 1u;
-        if (++st == kStages) { st = 0; ++round; }
       }
       if (++buf == 2) { buf = 0; ++buf_round; }
     }
@@ -496,7 +503,7 @@ grouped_mx4_kernel(const __grid_constant__ CUtensorMap map_x16, const __grid_con
       moe::mbar_wait(&s.drained, 0, 200000000ull);
     }
   } else if (warp == 1) {  // the pair's second CTA: tell the first that a stage is there
-    Tiles<CG> tl(a, s.first_tile);
+    Tiles<CG, kGate> tl(a, s.first_tile);
     int st = 0;
     uint32_t round = 0;
     bool ok = true;
@@ -515,7 +522,7 @@ grouped_mx4_kernel(const __grid_constant__ CUtensorMap map_x16, const __grid_con
   } else if (warp < 4) {
     // Scales: chunk 2 kb + (warp - 2) of each stage.  Lane l copies the words of rows l, 32 + l, 64 + l, 96 + l (of the
     // weights' tile, then of each 128 of x's) side by side; the copies (cp.async) complete on the stage's barrier.
-    Tiles<CG> tl(a, s.first_tile);
+    Tiles<CG, kGate> tl(a, s.first_tile);
     const int which = warp - 2;
     const int64_t w_rows = static_cast<int64_t>(a.E) * a.N;
     int st = 0;
@@ -568,7 +575,7 @@ grouped_mx4_kernel(const __grid_constant__ CUtensorMap map_x16, const __grid_con
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
-    Tiles<CG> tl(a, s.first_tile);
+    Tiles<CG, kGate> tl(a, s.first_tile);
     const int quad = warp & 3, turn = (warp - 4) >> 2;  // lanes 32 quad .. +31, column blocks turn, turn + 2, ...
     uint32_t buf = 0, buf_round = 0, half = 0;
     // a lane's place in a block: stmatrix writes 16 bytes of row j at chunk m, both swizzled as the store's map says
@@ -577,7 +584,7 @@ grouped_mx4_kernel(const __grid_constant__ CUtensorMap map_x16, const __grid_con
       if (!wait_warp(&s.acc_full[buf], buf_round & 1u, abort, a.status)) break;
       tmem_fence_after();
       const int cols = tl.cols();
-      const int col0 = a.gate ? tl.f * (kTileF / 2) + quad * 16 : tl.f * kTileF + quad * 32;
+      const int col0 = kGate ? tl.f * (kTileF / 2) + quad * 16 : tl.f * kTileF + quad * 32;
       for (int c0 = turn * kEpiT; c0 < cols; c0 += 2 * kEpiT) {
         uint32_t lo[16], hi[16];  // lanes 0..15 and 16..31: with the gate, gate and up
         const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * S::kTileT + c0;
@@ -589,7 +596,7 @@ grouped_mx4_kernel(const __grid_constant__ CUtensorMap map_x16, const __grid_con
         if (elect_one()) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");  // this half has been read
         __syncwarp();
         tmem_wait_ld();
-        if (a.gate) {  // 16 features, rows of 32 bytes: chunk ^= row / 4
+        if (kGate) {  // 16 features, rows of 32 bytes: chunk ^= row / 4
 #pragma unroll
           for (int i = 0; i < 4; i += 2) {
             uint32_t p[4];
@@ -628,11 +635,11 @@ grouped_mx4_kernel(const __grid_constant__ CUtensorMap map_x16, const __grid_con
         } else {  // the last rows of an expert: what follows is not this expert's to write
           __syncwarp();
           __nv_bfloat16* out = a.out + static_cast<int64_t>(tl.row0 + c0) * a.ld_out + col0;
-          const int shift = a.gate ? 1 : 2;  // log2 of a row's 16-byte chunks
+          constexpr int shift = kGate ? 1 : 2;  // log2 of a row's 16-byte chunks
           for (int i = lane; i < left << shift; i += 32) {
             const int j = i >> shift, g = i & ((1 << shift) - 1);
             if (col0 + g * 8 >= a.ld_out) continue;
-            const int at = a.gate ? j * 32 + ((g ^ ((j >> 2) & 1)) << 4) : j * 64 + ((g ^ ((j >> 1) & 3)) << 4);
+            const int at = kGate ? j * 32 + ((g ^ ((j >> 2) & 1)) << 4) : j * 64 + ((g ^ ((j >> 1) & 3)) << 4);
             moe::st_plain(reinterpret_cast<uint4*>(out + j * a.ld_out + g * 8), moe::lds128(epi + at));
           }
           if (elect_one()) moe::bulk_commit();  // (empty: a group a block)
@@ -725,18 +732,18 @@ bool out_map(CUtensorMap* m, void* out, int64_t rows, int64_t cols, bool gate) {
 
 constexpr int kPairRows = 64;  // rows an expert from which on pairs of CTAs take a tile
 
-template <int CG>
+template <int CG, bool kGate>
 moe_status_t launch_product(ProductArgs a, const CUtensorMap (&mx)[4], const CUtensorMap& mw,
                             const CUtensorMap& mo, cudaStream_t st) {
-  const int per = CG * (a.gate ? kTileF / 2 : kTileF);
+  const int per = CG * (kGate ? kTileF / 2 : kTileF);
   a.ftiles = static_cast<int>((a.ld_out + per - 1) / per);
   const int sms = moe_host::sm_count();
   if (sms <= 0) return MOE_ERR_CUDA;
   // no more CTAs than tiles there can be: a row tile per expert and per kTileT rows
-  const int64_t most = ((a.E < a.capacity ? a.E : a.capacity) + a.capacity / Shape<CG>::kTileT) * a.ftiles;
+  const int64_t most = ((a.E < a.capacity ? a.E : a.capacity) + a.capacity / Shape<CG, kGate>::kTileT) * a.ftiles;
   const int64_t grid = (most < sms / CG ? most : sms / CG) * CG;
-  const size_t smem = sizeof(typename Shape<CG>::Smem) + 1024;
-  const void* kernel = reinterpret_cast<const void*>(&grouped_mx4_kernel<CG>);
+  const size_t smem = sizeof(typename Shape<CG, kGate>::Smem) + 1024;
+  const void* kernel = reinterpret_cast<const void*>(&grouped_mx4_kernel<CG, kGate>);
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) !=
           cudaSuccess ||
       moe_host::prefer_max_shared(kernel) != cudaSuccess)
@@ -754,7 +761,7 @@ moe_status_t launch_product(ProductArgs a, const CUtensorMap (&mx)[4], const CUt
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = CG == 1 ? 1 : 2;
-  return cudaLaunchKernelEx(&cfg, grouped_mx4_kernel<CG>, mx[0], mx[1], mx[2], mx[3], mw, mo, a) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, grouped_mx4_kernel<CG, kGate>, mx[0], mx[1], mx[2], mx[3], mw, mo, a) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // namespace
@@ -786,7 +793,6 @@ extern "C" moe_status_t moe_grouped_gemm_mx4(const void* x_codes, const void* x_
   a.K = K;
   a.chunks = (K + 127) / 128;
   a.kstages = (K + kStageK - 1) / kStageK;
-  a.gate = gate ? 1 : 0;
   a.ld_out = gate ? N / 2 : N;
   a.capacity = capacity;
   a.out = static_cast<__nv_bfloat16*>(out);
@@ -796,12 +802,13 @@ extern "C" moe_status_t moe_grouped_gemm_mx4(const void* x_codes, const void* x_
   CUtensorMap mx[4], mw, mo;
   if (!out_map(&mo, out, capacity, a.ld_out, gate)) return MOE_ERR_CUDA;
   for (int i = 0; i < 4; ++i) {
-    const uint32_t box = i < 3 ? kBoxRows << i : pair ? Shape<2>::kRowsB : Shape<1>::kRowsB;
+    const uint32_t box = i < 3 ? kBoxRows << i : pair ? Shape<2, false>::kRowsB : Shape<1, false>::kRowsB;
     if (!codes_map(&mx[i], x_codes, capacity, K, box)) return MOE_ERR_CUDA;
   }
   if (!(a.gate_box ? gate_map(&mw, w_codes, E_local, N, K)
                    : codes_map(&mw, w_codes, static_cast<int64_t>(E_local) * N, K, gate ? kBoxRows : kTileF)))
     return MOE_ERR_CUDA;
-  return pair ? launch_product<2>(a, mx, mw, mo, static_cast<cudaStream_t>(stream))
-              : launch_product<1>(a, mx, mw, mo, static_cast<cudaStream_t>(stream));
+  const auto launch = pair ? (gate ? launch_product<2, true> : launch_product<2, false>)
+                           : (gate ? launch_product<1, true> : launch_product<1, false>);
+  return launch(a, mx, mw, mo, static_cast<cudaStream_t>(stream));
 }
