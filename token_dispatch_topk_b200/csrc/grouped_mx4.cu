@@ -86,6 +86,10 @@ struct ProductArgs {
   int32_t* status;
 };
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
 // x, 0, 0, group, expert: with the gate, four groups of 16 gate and the 16 matching up features
 __device__ __forceinline__ void tma_load_gate(void* dst, const CUtensorMap* map, int x, int group, int e, uint64_t* bar) {
   asm volatile("cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %3, %4, %5}], [%6];" ::"r"(
@@ -352,28 +356,29 @@ grouped_mx4_kernel(const __grid_constant__ CUtensorMap map_x16, const __grid_con
       asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
   }
+  if (warp == 0 && elect_one()) {
+    prefetch_map(&map_w);
+    prefetch_map(&map_x16);
+    prefetch_map(&map_x32);
+    prefetch_map(&map_x64);
+    prefetch_map(&map_x);
+    prefetch_map(&map_out);
+  }
   moe::pdl_launch_dependents();
   moe::pdl_wait();  // rows, scales, counts and offsets may come from the previous kernel
 
-  // row tiles before each expert: four experts a thread
-  {
-    constexpr int kPer = 4;
-    static_assert(kPer * 256 >= kMaxExperts, "experts a thread");
-    int n[kPer], sum = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int e = tid * kPer + i;
-      n[i] = 0;
-      if (e < a.E) {
-        const int64_t cnt = a.counts[e], off = a.offsets[e];
-        if (cnt < 0 || off < 0 || off + cnt > a.capacity)
-          moe::record_status(a.status, MOE_ERR_BAD_ROW);  // skipped
-        else
-          n[i] = static_cast<int>((cnt + S::kTileT - 1) / S::kTileT);
-      }
-      sum += n[i];
+  // row tiles before each expert: a scan, a thread per expert
+  for (int e0 = 0, before = 0; e0 < a.E; e0 += kThreads) {
+    const int ex = e0 + tid;
+    int n = 0;
+    if (ex < a.E) {
+      const int64_t cnt = a.counts[ex], off = a.offsets[ex];
+      if (cnt < 0 || off < 0 || off + cnt > a.capacity)
+        moe::record_status(a.status, MOE_ERR_BAD_ROW);  // skipped
+      else
+        n = static_cast<int>((cnt + S::kTileT - 1) / S::kTileT);
     }
-    int incl = sum;
+    int incl = n;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int o = __shfl_up_sync(0xffffffffu, incl, d);
@@ -381,15 +386,17 @@ grouped_mx4_kernel(const __grid_constant__ CUtensorMap map_x16, const __grid_con
     }
     if (lane == 31) s.warp_sums[warp] = incl;
     __syncthreads();
-    int before = incl - sum;
-    for (int w = 0; w < warp; ++w) before += s.warp_sums[w];
+    int all = 0, mine = 0;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int e = tid * kPer + i;
-      if (e <= a.E) s.first_tile[e] = before;  // (a.E <= 1024: thread 256 writes the last)
-      before += n[i];
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w == warp) mine = all;
+      all += s.warp_sums[w];
     }
+    if (ex < a.E) s.first_tile[ex + 1] = before + mine + incl;
+    before += all;
+    if (e0 + kThreads < a.E) __syncthreads();  // before the sums are written again
   }
+  if (tid == 0) s.first_tile[0] = 0;
   tmem_fence_before();
   __syncthreads();
   if constexpr (CG == 2) {  // the other CTA's barriers are initialised

@@ -179,7 +179,7 @@ gather_grad_kernel(const uint4* __restrict__ gp, const int32_t* __restrict__ inv
 
 // ---------------------------------------------------------------------------------------------- gating --
 constexpr int kGateWarps = 8;
-constexpr int kGateFloats = 1024;  // of shared memory a warp: the rows of a batch, and the most experts
+constexpr int kGateFloats = 1024;  // of shared memory a warp: the most experts of its 32 / G rows (G lanes a row)
 
 struct GateGradArgs {
   const float* gw;      // [T, k] incoming
@@ -189,7 +189,6 @@ struct GateGradArgs {
   int64_t T;
   int E, k;
   int renorm, sigmoid;
-  int rows;             // rows of a warp's batch
   int kp_log2;          // log2 of the lanes a row's slots take (k rounded up to a power of two)
   int g_log2;           // log2 of the lanes a row's logits take (dense)
   void* gx;             // [T, E] out
@@ -239,110 +238,147 @@ __device__ __forceinline__ float one_logit(const TX* p) {
   return v[0];
 }
 
-// A warp takes a batch of rows.  First its lanes take the rows' slots, several rows at once (their loads and the
-// scattered logits of the logistic are what the kernel waits for), and put the selected experts' values into the rows'
-// fp32 sums in shared memory; then the rows leave in order, 16 bytes a lane where E allows it (VEC), the dense softmax
-// gradient with the probabilities recomputed from CPL vectors of logits a lane, in one read.
-template <typename TX, int VEC, int CPL, bool kDense>
-__global__ void __launch_bounds__(kGateWarps * 32) gate_grad_kernel(GateGradArgs a) {
+// The slots of a few rows, kp lanes a row (k rounded up to a power of two): lane j of a row's lanes has selected expert
+// j.  value: what the expert's logit gets, complete in the lane that leads its expert (an expert named twice in a row
+// adds up, in slot order); G = sum_j g_j w_j of the row.
+struct Slots {
+  int id;       // -1: none
+  bool lead;
+  float value, G;
+};
+template <typename TX, bool kDense>
+__device__ __forceinline__ Slots take_slots(const GateGradArgs& a, int64_t t0, int r, int n, const TX* x, int lane) {
+  const int kp = 1 << a.kp_log2, j = lane & (kp - 1), base = lane & ~(kp - 1);
+  Slots s;
+  s.id = -1;
+  float g = 0.f, w = 0.f;
+  if (r < n && j < a.k) {
+    const int64_t at = (t0 + r) * a.k + j;
+    s.id = a.ids[at];
+    g = a.gw[at];
+    w = a.w[at];
+    if (s.id < 0 || s.id >= a.E) {
+      moe::record_status(a.status, MOE_ERR_BAD_EXPERT_ID);
+      s.id = -1;
+      g = w = 0.f;
+    }
+  }
+  float xs = 0.f;
+  if (!kDense && a.sigmoid && s.id >= 0) xs = one_logit(x + static_cast<int64_t>(r) * a.E + s.id);
+  s.G = g * w;
+  for (int d = kp >> 1; d > 0; d >>= 1) s.G += __shfl_xor_sync(0xffffffffu, s.G, d);
+  s.value = kDense ? g : a.renorm ? w * (g - s.G) : w * g;
+  const unsigned same = __match_any_sync(0xffffffffu, s.id >= 0 ? (r << 10) | s.id : -1 - lane);
+  s.lead = s.id >= 0 && __ffs(same) - 1 == lane;
+  if (!kDense && a.sigmoid) {
+    // all of a row's scores underflowed to 0: its weights are the constant 1/k
+    const unsigned some = __ballot_sync(0xffffffffu, s.id >= 0 && expf(-xs) < INFINITY);
+    const unsigned group = (kp == 32 ? 0xffffffffu : (1u << kp) - 1u) << base;
+    s.value = (some & group) != 0u ? s.value / (1.f + expf(xs)) : 0.f;
+  }
+  if (__any_sync(0xffffffffu, __popc(same) > 1)) {
+    const float mine = s.value;
+    for (int m = 1; m < kp; ++m) {
+      const float o = __shfl_sync(0xffffffffu, mine, base | ((j + m) & (kp - 1)));
+      if (j + m < kp && ((same >> (lane + m)) & 1u)) s.value += o;
+    }
+  }
+  return s;
+}
+
+// Only the selected experts' logits have a gradient: a warp takes as many rows as its lanes have room for their slots,
+// sends zeros to the rows at once, while the slots (and, for the logistic, the scattered logits) are on their way, and
+// then writes the selected elements over them.  Bound by the T E elements written and, for the logistic, by a DRAM
+// sector per selected logit.  65536 x 256 bf16, k = 8: 13.6 us; 16.7 us with the rows put together in shared
+// memory first.
+template <typename TX, int VEC>
+__global__ void __launch_bounds__(kGateWarps * 32) gate_grad_sparse_kernel(GateGradArgs a) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.E;
+  const int rows = 32 >> a.kp_log2;
+  const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kGateWarps + warp) * rows;
+  const int n = a.T - t0 < rows ? static_cast<int>(a.T - t0) : rows;
+  moe::pdl_launch_dependents();
+  moe::pdl_wait();
+  if (n <= 0) return;  // uniform per warp
+  const TX* x = static_cast<const TX*>(a.x) + t0 * E;
+  TX* gx = static_cast<TX*>(a.gx) + t0 * E;
+  const bool in_place = a.sigmoid && a.x == a.gx;  // the logits are read before they are written
+  const float zeros[VEC] = {};
+  if (!in_place)
+    for (int i = lane * VEC; i < n * E; i += 32 * VEC) RowVec<TX, VEC>::store(gx + i, zeros);
+  const int r = lane >> a.kp_log2;
+  const Slots s = take_slots<TX, false>(a, t0, r, n, x, lane);
+  __syncwarp();
+  if (in_place) {
+    for (int i = lane * VEC; i < n * E; i += 32 * VEC) RowVec<TX, VEC>::store(gx + i, zeros);
+    __syncwarp();
+  }
+  if (s.lead) {
+    const float v[1] = {s.value};
+    RowVec<TX, 1>::store(gx + r * E + s.id, v);
+  }
+}
+
+// The softmax over all experts: every logit has a gradient.  A row takes G lanes, CPL vectors each, read once and first
+// of all; the selected experts' g_j go into the row's fp32 sums in shared memory meanwhile; the probabilities are
+// recomputed.
+template <typename TX, int VEC, int CPL>
+__global__ void __launch_bounds__(kGateWarps * 32) gate_grad_dense_kernel(GateGradArgs a) {
   __shared__ __align__(16) float s_rows[kGateWarps][kGateFloats];
   __shared__ float s_sum[kGateWarps][32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.E;
   float* sums = s_rows[warp];
-  const int E = a.E, k = a.k;
-  const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kGateWarps + warp) * a.rows;
-  const int n = a.T - t0 < a.rows ? static_cast<int>(a.T - t0) : a.rows;  // may be 0 or less
+  const int G = 1 << a.g_log2, rows = 32 >> a.g_log2, l = lane & (G - 1), r = lane >> a.g_log2, chunks = E / VEC;
+  const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kGateWarps + warp) * rows;
+  const int n = a.T - t0 < rows ? static_cast<int>(a.T - t0) : rows;
   for (int i = lane * 4; i < n * E; i += 128) *reinterpret_cast<float4*>(sums + i) = make_float4(0.f, 0.f, 0.f, 0.f);
   moe::pdl_launch_dependents();
   moe::pdl_wait();
   if (n <= 0) return;  // uniform per warp
   const TX* x = static_cast<const TX*>(a.x) + t0 * E;
   TX* gx = static_cast<TX*>(a.gx) + t0 * E;
-  __syncwarp();
-  const int kp = 1 << a.kp_log2, j = lane & (kp - 1);
-  for (int r0 = 0; r0 < n; r0 += 32 >> a.kp_log2) {
-    const int r = r0 + (lane >> a.kp_log2);
-    int id = -1;
-    float g = 0.f, w = 0.f;
-    if (r < n && j < k) {
-      const int64_t s = (t0 + r) * k + j;
-      id = a.ids[s];
-      g = a.gw[s];
-      w = a.w[s];
-      if (id < 0 || id >= E) {
-        moe::record_status(a.status, MOE_ERR_BAD_EXPERT_ID);
-        id = -1;
-        g = w = 0.f;
-      }
-    }
-    float G = g * w;
-    for (int d = kp >> 1; d > 0; d >>= 1) G += __shfl_xor_sync(0xffffffffu, G, d);
-    float v = kDense ? g : a.renorm ? w * (g - G) : w * g;
-    if (!kDense && a.sigmoid) {
-      const float xs = id >= 0 ? one_logit(x + static_cast<int64_t>(r) * E + id) : 0.f;
-      // all of a row's scores underflowed to 0: its weights are the constant 1/k
-      const unsigned some = __ballot_sync(0xffffffffu, id >= 0 && expf(-xs) < INFINITY);
-      const unsigned group = (kp == 32 ? 0xffffffffu : (1u << kp) - 1u) << (lane & ~(kp - 1));
-      v = (some & group) != 0u ? v / (1.f + expf(xs)) : 0.f;
-    }
-    const unsigned same = __match_any_sync(0xffffffffu, id >= 0 ? (r << 10) | id : -1 - lane);
-    const bool lead = id >= 0 && __ffs(same) - 1 == lane;
-    if (__any_sync(0xffffffffu, __popc(same) > 1)) {  // an expert named twice in a row: add in slot order
-      const float mine = v;
-      for (int m = 1; m < kp; ++m) {
-        const float o = __shfl_sync(0xffffffffu, mine, (lane & ~(kp - 1)) | ((j + m) & (kp - 1)));
-        if (j + m < kp && ((same >> (lane + m)) & 1u)) v += o;
-      }
-    }
-    if (lead) sums[r * E + id] = v;
-    if (kDense && j == 0 && r < n) s_sum[warp][r] = G;
+  float v[CPL][VEC];
+#pragma unroll
+  for (int i = 0; i < CPL; ++i) {
+    const int c = l + i * G;
+#pragma unroll
+    for (int q = 0; q < VEC; ++q) v[i][q] = -INFINITY;
+    if (r < n && c < chunks) RowVec<TX, VEC>::load(x + r * E + c * VEC, v[i]);
   }
   __syncwarp();
-  if constexpr (kDense) {
-    const int G = 1 << a.g_log2, l = lane & (G - 1), chunks = E / VEC;
-    for (int r0 = 0; r0 < n; r0 += 32 >> a.g_log2) {
-      const int r = r0 + (lane >> a.g_log2);
-      float v[CPL][VEC];
-      float m = -INFINITY;
+  for (int r0 = 0; r0 < n; r0 += 32 >> a.kp_log2) {
+    const int rs = r0 + (lane >> a.kp_log2);
+    const Slots s = take_slots<TX, true>(a, t0, rs, n, x, lane);
+    if (s.lead) sums[rs * E + s.id] = s.value;
+    if ((lane & ((1 << a.kp_log2) - 1)) == 0 && rs < n) s_sum[warp][rs] = s.G;
+  }
+  float m = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < CPL; ++i) {
-        const int c = l + i * G;
+  for (int i = 0; i < CPL; ++i)
 #pragma unroll
-        for (int q = 0; q < VEC; ++q) v[i][q] = -INFINITY;
-        if (r < n && c < chunks) RowVec<TX, VEC>::load(x + r * E + c * VEC, v[i]);
+    for (int q = 0; q < VEC; ++q) m = fmaxf(m, v[i][q]);
+  for (int d = G >> 1; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  float z = 0.f;
 #pragma unroll
-        for (int q = 0; q < VEC; ++q) m = fmaxf(m, v[i][q]);
-      }
-      for (int d = G >> 1; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-      float z = 0.f;
+  for (int i = 0; i < CPL; ++i)
 #pragma unroll
-      for (int i = 0; i < CPL; ++i)
-#pragma unroll
-        for (int q = 0; q < VEC; ++q) {
-          v[i][q] = expf(v[i][q] - m);
-          if (r < n && l + i * G < chunks) z += v[i][q];
-        }
-      for (int d = G >> 1; d > 0; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
-      z = 1.f / z;
-      if (r < n) {
-        const float mean = s_sum[warp][r];
-#pragma unroll
-        for (int i = 0; i < CPL; ++i) {
-          const int c = l + i * G;
-          if (c < chunks) {
-#pragma unroll
-            for (int q = 0; q < VEC; ++q) v[i][q] = v[i][q] * z * (sums[r * E + c * VEC + q] - mean);
-            RowVec<TX, VEC>::store(gx + r * E + c * VEC, v[i]);
-          }
-        }
-      }
+    for (int q = 0; q < VEC; ++q) {
+      v[i][q] = expf(v[i][q] - m);
+      if (r < n && l + i * G < chunks) z += v[i][q];
     }
-  } else {
-    for (int i = lane * VEC; i < n * E; i += 32 * VEC) {
-      float v[VEC];
+  for (int d = G >> 1; d > 0; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
+  z = 1.f / z;
+  __syncwarp();
+  if (r < n) {
+    const float mean = s_sum[warp][r];
 #pragma unroll
-      for (int q = 0; q < VEC; ++q) v[q] = sums[i + q];
-      RowVec<TX, VEC>::store(gx + i, v);
+    for (int i = 0; i < CPL; ++i) {
+      const int c = l + i * G;
+      if (c < chunks) {
+#pragma unroll
+        for (int q = 0; q < VEC; ++q) v[i][q] = v[i][q] * z * (sums[r * E + c * VEC + q] - mean);
+        RowVec<TX, VEC>::store(gx + r * E + c * VEC, v[i]);
+      }
     }
   }
 }
@@ -354,14 +390,14 @@ using GateKernel = void (*)(GateGradArgs);
 template <typename TX, int VEC>
 GateKernel dense_kernel(int cpl) {
   if constexpr (VEC == 8) {
-    return cpl <= 1 ? gate_grad_kernel<TX, 8, 1, true>
-                    : cpl <= 2 ? gate_grad_kernel<TX, 8, 2, true> : gate_grad_kernel<TX, 8, 4, true>;
+    return cpl <= 1 ? gate_grad_dense_kernel<TX, 8, 1>
+                    : cpl <= 2 ? gate_grad_dense_kernel<TX, 8, 2> : gate_grad_dense_kernel<TX, 8, 4>;
   } else if constexpr (VEC == 4) {
-    return cpl <= 1 ? gate_grad_kernel<TX, 4, 1, true>
-                    : cpl <= 2 ? gate_grad_kernel<TX, 4, 2, true> : gate_grad_kernel<TX, 4, 8, true>;
+    return cpl <= 1 ? gate_grad_dense_kernel<TX, 4, 1>
+                    : cpl <= 2 ? gate_grad_dense_kernel<TX, 4, 2> : gate_grad_dense_kernel<TX, 4, 8>;
   } else {
-    return cpl <= 2 ? gate_grad_kernel<TX, 1, 2, true>
-                    : cpl <= 8 ? gate_grad_kernel<TX, 1, 8, true> : gate_grad_kernel<TX, 1, 32, true>;
+    return cpl <= 2 ? gate_grad_dense_kernel<TX, 1, 2>
+                    : cpl <= 8 ? gate_grad_dense_kernel<TX, 1, 8> : gate_grad_dense_kernel<TX, 1, 32>;
   }
 }
 
@@ -376,17 +412,13 @@ moe_status_t launch_gate_grad(GateGradArgs a, cudaStream_t st) {
   a.g_log2 = 0;
   while ((1 << a.g_log2) < chunks && a.g_log2 < 5) ++a.g_log2;
   const int cpl = (chunks + 31) / 32;
-  // rows of a batch: as many as fit a warp's shared memory, fewer where that would leave the SMs fewer than 16 warps
-  const int sms = moe_host::sm_count();
-  if (sms <= 0) return MOE_ERR_CUDA;
-  a.rows = 1;
-  while (a.rows < 32 && 2 * a.rows * a.E <= kGateFloats && a.T >= int64_t{2} * a.rows * sms * 16) a.rows *= 2;
+  const int rows = 32 >> (dense ? a.g_log2 : a.kp_log2);
   GateKernel kernel;
-  if (wide)
-    kernel = dense ? dense_kernel<TX, kWide>(cpl) : static_cast<GateKernel>(gate_grad_kernel<TX, kWide, 1, false>);
+  if (dense)
+    kernel = wide ? dense_kernel<TX, kWide>(cpl) : dense_kernel<TX, 1>(cpl);
   else
-    kernel = dense ? dense_kernel<TX, 1>(cpl) : static_cast<GateKernel>(gate_grad_kernel<TX, 1, 1, false>);
-  const int64_t batches = (a.T + a.rows - 1) / a.rows;
+    kernel = wide ? gate_grad_sparse_kernel<TX, kWide> : gate_grad_sparse_kernel<TX, 1>;
+  const int64_t batches = (a.T + rows - 1) / rows;
   return moe_host::launch_pdl(kernel, dim3(static_cast<unsigned>((batches + kGateWarps - 1) / kGateWarps)),
                               dim3(kGateWarps * 32), 0, st, a);
 }
