@@ -114,67 +114,75 @@ __global__ void __launch_bounds__(kWarps * 32) combine_grad_kernel(CombineGradAr
 }
 
 // ---------------------------------------------------------------------------------------------- gather --
-// grad_hidden[t] = the sum of the token's local rows.  A warp takes kSumVecs vectors a lane of one token's rows and
-// adds the rows kSumRows at a time, their loads in flight together.  Rows that are not there (other ranks' experts)
-// cost nothing, which the combine's ring of fixed k-row stages cannot offer.
-constexpr int kSumVecs = 2, kSumRows = 4;
+// grad_hidden[t] = the sum of the token's local rows.  A warp takes kSumVecs vectors a lane of `per` tokens, whose slots
+// its lanes read at once, and adds a token's rows kSumRows at a time, their loads in flight together.  Rows that are
+// not there (other ranks' experts) cost nothing, which the combine's ring of fixed k-row stages cannot offer (one of
+// four ranks, 16384 x 6 x 4096: 113 us by that kernel, 56 by this one; 4096 x 8 x 2048, all rows there: 26 and 21).
+// Several tokens a warp, two rows at a time, are for sparse rows (one of eight ranks, 65536 x 8 x 2048: 89 us against
+// 117 with one token and four rows) and cost full ones 4 % (16384 x 8 x 7168: 321 against 308, 323 at the copy rate).
+constexpr int kSumVecs = 2;
 
+template <int kSumRows, bool kOne>  // kOne: one token a warp
 __global__ void __launch_bounds__(kWarps * 32)
-gather_grad_kernel(const uint4* __restrict__ gp, const int32_t* __restrict__ inv_perm, int64_t T, int k, int nv,
-                   int segs, int64_t capacity, uint4* __restrict__ gx, int32_t* status) {
+gather_grad_kernel(const uint4* __restrict__ gp, const int32_t* __restrict__ inv_perm, int64_t T, int k, int per,
+                   int nv, int segs, int64_t capacity, uint4* __restrict__ gx, int32_t* status) {
   moe::pdl_launch_dependents();
   moe::pdl_wait();
   const int lane = threadIdx.x & 31;
   const int64_t wid = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  const int64_t t = wid / segs;
-  if (t >= T) return;
+  const int64_t group = wid / segs, t0 = kOne ? group : group * per;
+  if (t0 >= T) return;
+  const int n = kOne ? 1 : T - t0 < per ? static_cast<int>(T - t0) : per;
   int r = -1;
-  if (lane < k) {
-    r = inv_perm[t * k + lane];
+  if (lane < n * k) {
+    r = inv_perm[t0 * k + lane];
     if (r < -1 || static_cast<int64_t>(r) >= capacity) {
       moe::record_status(status, MOE_ERR_BAD_ROW);
       r = -1;
     }
   }
-  const int v0 = static_cast<int>(wid - t * segs) * (32 * kSumVecs) + lane;
-  float acc[kSumVecs][8];
+  const unsigned local = __ballot_sync(0xffffffffu, r >= 0);
+  const int v0 = static_cast<int>(wid - group * segs) * (32 * kSumVecs) + lane;
+  for (int i = 0; i < n; ++i) {
+    float acc[kSumVecs][8];
 #pragma unroll
-  for (int u = 0; u < kSumVecs; ++u)
+    for (int u = 0; u < kSumVecs; ++u)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[u][i] = 0.f;
-  unsigned left = __ballot_sync(0xffffffffu, r >= 0);
-  while (left != 0u) {
-    uint4 in[kSumRows][kSumVecs];
+      for (int q = 0; q < 8; ++q) acc[u][q] = 0.f;
+    unsigned left = kOne || k == 32 ? local : local & (((1u << k) - 1u) << (i * k));
+    while (left != 0u) {
+      uint4 in[kSumRows][kSumVecs];
 #pragma unroll
-    for (int q = 0; q < kSumRows; ++q) {
+      for (int q = 0; q < kSumRows; ++q) {
 #pragma unroll
-      for (int u = 0; u < kSumVecs; ++u) in[q][u] = make_uint4(0u, 0u, 0u, 0u);
-      if (left != 0u) {  // uniform; ascending slot order
-        const int64_t row = __shfl_sync(0xffffffffu, r, __ffs(left) - 1);
-        left &= left - 1u;
+        for (int u = 0; u < kSumVecs; ++u) in[q][u] = make_uint4(0u, 0u, 0u, 0u);
+        if (left != 0u) {  // uniform; ascending slot order
+          const int64_t row = __shfl_sync(0xffffffffu, r, __ffs(left) - 1);
+          left &= left - 1u;
 #pragma unroll
-        for (int u = 0; u < kSumVecs; ++u)
-          if (v0 + 32 * u < nv) in[q][u] = moe::ld_stream(gp + row * nv + v0 + 32 * u);
-      }
-    }
-#pragma unroll
-    for (int q = 0; q < kSumRows; ++q)  // (a row that is not there adds +0, which changes no sum)
-#pragma unroll
-      for (int u = 0; u < kSumVecs; ++u) {
-        const uint32_t x[4] = {in[q][u].x, in[q][u].y, in[q][u].z, in[q][u].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          acc[u][2 * i] += moe::bf16_lo(x[i]);
-          acc[u][2 * i + 1] += moe::bf16_hi(x[i]);
+          for (int u = 0; u < kSumVecs; ++u)
+            if (v0 + 32 * u < nv) in[q][u] = moe::ld_stream(gp + row * nv + v0 + 32 * u);
         }
       }
-  }
 #pragma unroll
-  for (int u = 0; u < kSumVecs; ++u)
-    if (v0 + 32 * u < nv)
-      moe::st_plain(gx + t * nv + v0 + 32 * u,
-                    make_uint4(moe::pack_bf16x2(acc[u][0], acc[u][1]), moe::pack_bf16x2(acc[u][2], acc[u][3]),
-                               moe::pack_bf16x2(acc[u][4], acc[u][5]), moe::pack_bf16x2(acc[u][6], acc[u][7])));
+      for (int q = 0; q < kSumRows; ++q)  // (a row that is not there adds +0, which changes no sum)
+#pragma unroll
+        for (int u = 0; u < kSumVecs; ++u) {
+          const uint32_t x[4] = {in[q][u].x, in[q][u].y, in[q][u].z, in[q][u].w};
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            acc[u][2 * w] += moe::bf16_lo(x[w]);
+            acc[u][2 * w + 1] += moe::bf16_hi(x[w]);
+          }
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < kSumVecs; ++u)
+      if (v0 + 32 * u < nv)
+        moe::st_plain(gx + (t0 + i) * nv + v0 + 32 * u,
+                      make_uint4(moe::pack_bf16x2(acc[u][0], acc[u][1]), moe::pack_bf16x2(acc[u][2], acc[u][3]),
+                                 moe::pack_bf16x2(acc[u][4], acc[u][5]), moe::pack_bf16x2(acc[u][6], acc[u][7])));
+  }
 }
 
 // ---------------------------------------------------------------------------------------------- gating --
@@ -511,10 +519,16 @@ extern "C" moe_status_t moe_gather_backward(const void* grad_permuted, const int
     return MOE_ERR_INVALID_ARG;
   if (!moe_host::aligned16(grad_permuted) || !moe_host::aligned16(grad_hidden)) return MOE_ERR_INVALID_ARG;
   const int nv = H / 8, segs = (nv + 32 * kSumVecs - 1) / (32 * kSumVecs);
-  const int64_t grid = (T * segs + kWarps - 1) / kWarps;
+  // tokens a warp: up to four, as far as that leaves every SM 64 warps
+  const int sms = moe_host::sm_count();
+  if (sms <= 0) return MOE_ERR_CUDA;
+  int per = 1;
+  while (per < 4 && 2 * per * k <= 32 && T * segs >= int64_t{2} * per * sms * 64) per *= 2;
+  const int64_t grid = ((T + per - 1) / per * segs + kWarps - 1) / kWarps;
   if (grid > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
-  return moe_host::launch_pdl(gather_grad_kernel, dim3(static_cast<unsigned>(grid)), dim3(kWarps * 32), 0,
+  const auto kernel = per == 1 ? gather_grad_kernel<4, true> : gather_grad_kernel<2, false>;
+  return moe_host::launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(kWarps * 32), 0,
                               static_cast<cudaStream_t>(stream), static_cast<const uint4*>(grad_permuted), inv_perm, T,
-                              static_cast<int>(k), nv, segs, capacity, static_cast<uint4*>(grad_hidden),
+                              static_cast<int>(k), per, nv, segs, capacity, static_cast<uint4*>(grad_hidden),
                               device_status);
 }
