@@ -411,7 +411,8 @@ MOE_API moe_status_t moe_gather_mx4(const void* hidden, int64_t T, int32_t H, in
  *   Products are exact, sums fp32 in the tensor cores.  A NaN block of a row makes that row NaN, of a weight row that
  *   feature.  Deterministic.
  *   An expert whose rows do not lie in [0, capacity) is skipped and MOE_ERR_BAD_ROW recorded in device_status (a
- *   device int32 or NULL); the experts' row ranges must not overlap.
+ *   device int32 or NULL).  The experts' row ranges must not overlap; counts that sum to well over capacity are refused
+ *   the same way, and nothing is written.
  *   Errors: INVALID_ARG (sizes, N % 8 != 0 or N % 16 with the gate, K % 32, N or K beyond 2^20, null or misaligned
  *   pointers), UNSUPPORTED (E_local > 1024).
  */

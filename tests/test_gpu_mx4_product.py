@@ -143,6 +143,10 @@ def test_bad_counts_and_offsets_are_skipped_and_recorded():
     tdt.moe_grouped_gemm_mx4(x, w, bad_c.cuda(), bad_o.cuda(), out=out, device_status=status)
     assert tdt.moe_read_status(status) == tdt.MOE_ERR_BAD_ROW
     assert torch.equal(out[:10], good[:10]) and (out[10:] == 77.0).all()
+    # every expert claims every row: too many to be ranges of their own
+    all_c, all_o = torch.full_like(counts, cap), torch.zeros_like(off)
+    tdt.moe_grouped_gemm_mx4(x, w, all_c.cuda(), all_o.cuda(), out=out.fill_(77.0), device_status=status)
+    assert (out == 77.0).all() and tdt.moe_read_status(status) == tdt.MOE_ERR_BAD_ROW
     # no expert has a row
     tdt.moe_grouped_gemm_mx4(x, w, torch.zeros_like(counts).cuda(), off.cuda(), out=out.fill_(77.0), device_status=status)
     assert (out == 77.0).all() and tdt.moe_read_status(status) == tdt.MOE_OK

@@ -26,7 +26,8 @@ REFUSED = [
      dict(inv_perm=None), dict(expert_out=None), dict(grad_out=ODD), dict(expert_out=ODD), dict(gy=ODD),
      dict(T=1 << 30), dict(capacity=1 << 31), dict(flags=2, sorted_ids=P, n_pad=P, gy=None)]),
     ("moe_combine_backward", COMBINE, UNSUPPORTED, [dict(k=33)]),
-    ("moe_combine_backward", COMBINE, OK, [dict(T=0)]),
+    ("moe_combine_backward", COMBINE, OK, [dict(T=0), dict(T=0, grad_out=None, topk_weights=None, inv_perm=None, gw=None),
+     dict(T=0, capacity=0, gy=None, gw=None, expert_out=None)]),
     ("moe_gather_backward", GATHER, INVALID, [dict(T=-1), dict(k=0), dict(H=0), dict(H=12), dict(capacity=-1),
      dict(gp=None), dict(inv_perm=None), dict(gx=None), dict(gp=ODD), dict(gx=ODD), dict(T=1 << 30)]),
     ("moe_gather_backward", GATHER, UNSUPPORTED, [dict(k=33)]),

@@ -63,6 +63,8 @@ struct Shape {
     uint8_t epi[kEpiWarps][2][kEpiBytes];
     int32_t first_tile[kMaxExperts + 1];  // row tiles before expert e
     int32_t warp_sums[kThreads / 32];
+    float warp_rows[kThreads / 32];
+    int tiles;
     uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drained;
     uint32_t tmem;
     int abort;
@@ -282,8 +284,8 @@ struct Tiles {
   int turn = 32;         // lane that holds the next tile
   int2 mine;             // this lane's tile
 
-  __device__ __forceinline__ Tiles(const ProductArgs& args, const int32_t* first_tile)
-      : a(args), first(first_tile), at(blockIdx.x / CG), total(first_tile[args.E] * args.ftiles) {}
+  __device__ __forceinline__ Tiles(const ProductArgs& args, const int32_t* first_tile, int tiles)
+      : a(args), first(first_tile), at(blockIdx.x / CG), total(tiles) {}
   __device__ __forceinline__ bool next() {
     if (at >= total) return false;
     if (turn == 32) {
@@ -368,35 +370,53 @@ grouped_mx4_kernel(const __grid_constant__ CUtensorMap map_x16, const __grid_con
   moe::pdl_wait();  // rows, scales, counts and offsets may come from the previous kernel
 
   // row tiles before each expert: a scan, a thread per expert
-  for (int e0 = 0, before = 0; e0 < a.E; e0 += kThreads) {
+  float all_rows = 0.f;
+  int before = 0;
+  for (int e0 = 0; e0 < a.E; e0 += kThreads) {
     const int ex = e0 + tid;
     int n = 0;
+    float rows = 0.f;
     if (ex < a.E) {
       const int64_t cnt = a.counts[ex], off = a.offsets[ex];
-      if (cnt < 0 || off < 0 || off + cnt > a.capacity)
+      if (cnt < 0 || off < 0 || off + cnt > a.capacity) {
         moe::record_status(a.status, MOE_ERR_BAD_ROW);  // skipped
-      else
+      } else {
         n = static_cast<int>((cnt + S::kTileT - 1) / S::kTileT);
+        rows = static_cast<float>(cnt);
+      }
     }
     int incl = n;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int o = __shfl_up_sync(0xffffffffu, incl, d);
       if (lane >= d) incl += o;
+      rows += __shfl_xor_sync(0xffffffffu, rows, d);
     }
-    if (lane == 31) s.warp_sums[warp] = incl;
+    if (lane == 31) {
+      s.warp_sums[warp] = incl;
+      s.warp_rows[warp] = rows;
+    }
     __syncthreads();
     int all = 0, mine = 0;
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
       if (w == warp) mine = all;
       all += s.warp_sums[w];
+      all_rows += s.warp_rows[w];
     }
     if (ex < a.E) s.first_tile[ex + 1] = before + mine + incl;
     before += all;
     if (e0 + kThreads < a.E) __syncthreads();  // before the sums are written again
   }
-  if (tid == 0) s.first_tile[0] = 0;
+  if (tid == 0) {
+    s.first_tile[0] = 0;
+    s.tiles = before * a.ftiles;
+    // ranges that overlap so much that the tiles might not fit an int: nothing is done (the sum's rounding is far less)
+    if (all_rows > 1.001f * static_cast<float>(a.capacity) + 1.f) {
+      moe::record_status(a.status, MOE_ERR_BAD_ROW);
+      s.tiles = 0;
+    }
+  }
   tmem_fence_before();
   __syncthreads();
   if constexpr (CG == 2) {  // the other CTA's barriers are initialised
@@ -408,7 +428,7 @@ grouped_mx4_kernel(const __grid_constant__ CUtensorMap map_x16, const __grid_con
   volatile int* abort = &s.abort;
 
   if (warp == 0) {
-    Tiles<CG, kGate> tl(a, s.first_tile);
+    Tiles<CG, kGate> tl(a, s.first_tile, s.tiles);
     int st = 0;
     uint32_t round = 0;
     int64_t issued = 0;
@@ -454,7 +474,7 @@ grouped_mx4_kernel(const __grid_constant__ CUtensorMap map_x16, const __grid_con
   } else if (warp == 1 && rank == 0) {
     // instruction descriptor: A and B e2m1, scales e8m0, 128 lanes a CTA; columns and scale ids below
     constexpr uint32_t kDesc = (1u << 7) | (1u << 10) | (1u << 23) | ((CG * 128u >> 4) << 24);
-    Tiles<CG, kGate> tl(a, s.first_tile);
+    Tiles<CG, kGate> tl(a, s.first_tile, s.tiles);
     const uint64_t da0 = desc_sw128(moe::smem_addr(s.ab[0])), sf0 = desc_plain(moe::smem_addr(s.sf[0]));
     int st = 0, st2 = 0;  // the stage, and the one two before it
     uint32_t round = 0, round2 = 0, buf = 0, buf_round = 0, set = 0;
@@ -510,7 +530,7 @@ grouped_mx4_kernel(const __grid_constant__ CUtensorMap map_x16, const __grid_con
       moe::mbar_wait(&s.drained, 0, 200000000ull);
     }
   } else if (warp == 1) {  // the pair's second CTA: tell the first that a stage is there
-    Tiles<CG, kGate> tl(a, s.first_tile);
+    Tiles<CG, kGate> tl(a, s.first_tile, s.tiles);
     int st = 0;
     uint32_t round = 0;
     bool ok = true;
@@ -529,7 +549,7 @@ grouped_mx4_kernel(const __grid_constant__ CUtensorMap map_x16, const __grid_con
   } else if (warp < 4) {
     // Scales: chunk 2 kb + (warp - 2) of each stage.  Lane l copies the words of rows l, 32 + l, 64 + l, 96 + l (of the
     // weights' tile, then of each 128 of x's) side by side; the copies (cp.async) complete on the stage's barrier.
-    Tiles<CG, kGate> tl(a, s.first_tile);
+    Tiles<CG, kGate> tl(a, s.first_tile, s.tiles);
     const int which = warp - 2;
     const int64_t w_rows = static_cast<int64_t>(a.E) * a.N;
     int st = 0;
@@ -582,7 +602,7 @@ grouped_mx4_kernel(const __grid_constant__ CUtensorMap map_x16, const __grid_con
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
-    Tiles<CG, kGate> tl(a, s.first_tile);
+    Tiles<CG, kGate> tl(a, s.first_tile, s.tiles);
     const int quad = warp & 3, turn = (warp - 4) >> 2;  // lanes 32 quad .. +31, column blocks turn, turn + 2, ...
     uint32_t buf = 0, buf_round = 0, half = 0;
     // a lane's place in a block: stmatrix writes 16 bytes of row j at chunk m, both swizzled as the store's map says

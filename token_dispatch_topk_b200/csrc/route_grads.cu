@@ -444,11 +444,11 @@ extern "C" moe_status_t moe_combine_backward(const void* grad_out, const void* e
   if ((flags & ~MOE_GATHER_ZERO_PAD) != 0u) return MOE_ERR_INVALID_ARG;
   if (T > (int64_t{1} << 40) || T * k >= (int64_t{1} << 30) || capacity >= (int64_t{1} << 31))
     return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;  // no slots, and with them no blocks to pad
   if (grad_expert_out == nullptr && grad_topk_weights == nullptr) return MOE_ERR_INVALID_ARG;
   const bool zero_pad = (flags & MOE_GATHER_ZERO_PAD) != 0u;
   if (zero_pad && (sorted_token_ids == nullptr || num_tokens_post_pad == nullptr || grad_expert_out == nullptr))
     return MOE_ERR_INVALID_ARG;
-  if (T == 0) return MOE_OK;  // no slots, and with them no blocks to pad
   if (grad_out == nullptr || topk_weights == nullptr || inv_perm == nullptr) return MOE_ERR_INVALID_ARG;
   if (capacity > 0 && grad_topk_weights != nullptr && expert_out == nullptr) return MOE_ERR_INVALID_ARG;
   if (!moe_host::aligned16(grad_out) || !moe_host::aligned16(expert_out) || !moe_host::aligned16(grad_expert_out))
