@@ -395,6 +395,14 @@ def _arg(t, name: str, dtype, shape, index: int) -> int:
     raise ValueError(f"{name} must be contiguous")
 
 
+def _out(t, name: str, dtype, shape, like: torch.Tensor):
+    """An output and its address: t, checked, or a new tensor on `like`'s device."""
+    if t is None:
+        t = like.new_empty(shape, dtype=dtype)
+        return t, t.data_ptr()
+    return t, _arg(t, name, dtype, shape, like.get_device())
+
+
 def _matrix(t, name: str):
     if t is None or t.dim() != 2:
         raise ValueError(f"{name} must be a matrix")
@@ -445,10 +453,8 @@ def moe_combine_backward(grad_out: torch.Tensor, expert_out: torch.Tensor, topk_
     k = _matrix(topk_weights, "topk_weights")[1]
     capacity = _matrix(expert_out, "expert_out")[0]
     dev, bf16 = grad_out.get_device(), torch.bfloat16
-    if grad_expert_out is None:
-        grad_expert_out = torch.empty((capacity, H), dtype=bf16, device=grad_out.device)
-    if grad_topk_weights is None:
-        grad_topk_weights = torch.empty((T, k), dtype=torch.float32, device=grad_out.device)
+    grad_expert_out, gy = _out(grad_expert_out, "grad_expert_out", bf16, (capacity, H), grad_out)
+    grad_topk_weights, gw = _out(grad_topk_weights, "grad_topk_weights", torch.float32, (T, k), grad_out)
     pads = (None, None)
     if zero_pad:
         pads = (_arg(sorted_token_ids, "sorted_token_ids", torch.int32, (capacity,), dev),
@@ -457,9 +463,7 @@ def moe_combine_backward(grad_out: torch.Tensor, expert_out: torch.Tensor, topk_
           _arg(expert_out, "expert_out", bf16, (capacity, H), dev),
           _arg(topk_weights, "topk_weights", torch.float32, (T, k), dev),
           _arg(inv_perm, "inv_perm", torch.int32, (T * k,), dev), *pads, T, k, H, capacity,
-          MOE_GATHER_ZERO_PAD if zero_pad else 0,
-          _arg(grad_expert_out, "grad_expert_out", bf16, (capacity, H), dev),
-          _arg(grad_topk_weights, "grad_topk_weights", torch.float32, (T, k), dev), _status_arg(device_status, dev))
+          MOE_GATHER_ZERO_PAD if zero_pad else 0, gy, gw, _status_arg(device_status, dev))
     return grad_expert_out, grad_topk_weights
 
 
@@ -472,11 +476,10 @@ def moe_gather_backward(grad_permuted: torch.Tensor, inv_perm: torch.Tensor, k: 
     if k < 1 or inv_perm.numel() % k != 0:
         raise ValueError(f"inv_perm must hold T * k slots, got {inv_perm.numel()} with k = {k}")
     T, dev = inv_perm.numel() // k, grad_permuted.get_device()
-    if grad_hidden is None:
-        grad_hidden = torch.empty((T, H), dtype=torch.bfloat16, device=grad_permuted.device)
+    grad_hidden, gx = _out(grad_hidden, "grad_hidden", torch.bfloat16, (T, H), grad_permuted)
     _call("moe_gather_backward", dev, stream,
           _arg(grad_permuted, "grad_permuted", torch.bfloat16, (capacity, H), dev),
-          _arg(inv_perm, "inv_perm", torch.int32, (T * k,), dev), T, k, H, capacity, _arg(grad_hidden, "grad_hidden", torch.bfloat16, (T, H), dev), _status_arg(device_status, dev))
+          _arg(inv_perm, "inv_perm", torch.int32, (T * k,), dev), T, k, H, capacity, gx, _status_arg(device_status, dev))
     return grad_hidden
 
 
@@ -491,14 +494,13 @@ def moe_topk_softmax_backward(grad_topk_weights: torch.Tensor, logits: torch.Ten
     dev, dtype = logits.get_device(), logits.dtype
     if dtype not in (torch.bfloat16, torch.float32):
         raise ValueError(f"logits dtype {dtype} unsupported (bf16 or fp32)")
-    if grad_logits is None:
-        grad_logits = torch.empty((T, E), dtype=dtype, device=logits.device)
+    grad_logits, gx = _out(grad_logits, "grad_logits", dtype, (T, E), logits)
     f32 = torch.float32
     _call("moe_topk_softmax_backward", dev, stream, _arg(grad_topk_weights, "grad_topk_weights", f32, (T, k), dev),
           _arg(logits, "logits", dtype, (T, E), dev), MOE_DTYPE_BF16 if dtype == torch.bfloat16 else MOE_DTYPE_F32,
           _arg(topk_weights, "topk_weights", f32, (T, k), dev), _arg(topk_ids, "topk_ids", torch.int32, (T, k), dev), T,
           E, k, (MOE_RENORMALIZE if renormalize else 0) | _scoring_flag(scoring),
-          _arg(grad_logits, "grad_logits", dtype, (T, E), dev), _status_arg(device_status, dev))
+          gx, _status_arg(device_status, dev))
     return grad_logits
 
 
@@ -529,12 +531,17 @@ def _mx4_args(q: Mx4Tensor, codes_name: str, scales_name: str, index: int):
             _arg(q.scales, scales_name, torch.uint8, ((half + 63) // 64, rows, 4), index))
 
 
-def _mx4_out(out: Optional[Mx4Tensor], rows: int, K: int, device) -> Mx4Tensor:
+def _mx4_out(out: Optional[Mx4Tensor], rows: int, K: int, like: torch.Tensor):
+    """An output in the format and its addresses: `out`, checked, or a new one on `like`'s device."""
     if out is None:
-        return alloc_mx4(rows, K, device)
+        if K < 32 or K % 32 != 0:
+            raise ValueError(f"a row holds whole blocks of 32 elements, got K = {K}")
+        out = Mx4Tensor(like.new_empty((rows, K // 2), dtype=torch.uint8),
+                        like.new_empty((-(-K // 128), rows, 4), dtype=torch.uint8))
+        return out, out.codes.data_ptr(), out.scales.data_ptr()
     if (out.rows, out.K) != (rows, K):
         raise ValueError(f"out holds [{out.rows}, {out.K}], [{rows}, {K}] is needed")
-    return out
+    return (out, *_mx4_args(out, "out.codes", "out.scales", like.get_device()))
 
 
 def moe_quantize_mx4(x: torch.Tensor, out: Optional[Mx4Tensor] = None, num_rows: Optional[torch.Tensor] = None,
@@ -542,21 +549,18 @@ def moe_quantize_mx4(x: torch.Tensor, out: Optional[Mx4Tensor] = None, num_rows:
     """x [rows, K] bf16 -> microscaled 4-bit floating point (K a multiple of 32).  num_rows (int32 [1] on the device):
     rows from there on are neither read nor written."""
     rows, K = _matrix(x, "x")
-    out = _mx4_out(out, rows, K, x.device)
+    out, codes, scales = _mx4_out(out, rows, K, x)
     dev = x.get_device()
     _call("moe_quantize_mx4", dev, stream, _arg(x, "x", torch.bfloat16, (rows, K), dev), rows, K,
-          None if num_rows is None else _arg(num_rows, "num_rows", torch.int32, (1,), dev),
-          *_mx4_args(out, "out.codes", "out.scales", dev))
+          None if num_rows is None else _arg(num_rows, "num_rows", torch.int32, (1,), dev), codes, scales)
     return out
 
 
 def moe_dequantize_mx4(q: Mx4Tensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The values of q as bf16 [rows, K]."""
-    dev, rows, K = q.codes.get_device(), q.rows, q.K
-    if out is None:
-        out = torch.empty((rows, K), dtype=torch.bfloat16, device=q.codes.device)
-    _call("moe_dequantize_mx4", dev, stream, *_mx4_args(q, "q.codes", "q.scales", dev), rows, K,
-          _arg(out, "out", torch.bfloat16, (rows, K), dev))
+    dev, (rows, half) = q.codes.get_device(), _matrix(q.codes, "q.codes")
+    out, p = _out(out, "out", torch.bfloat16, (rows, 2 * half), q.codes)
+    _call("moe_dequantize_mx4", dev, stream, *_mx4_args(q, "q.codes", "q.scales", dev), rows, 2 * half, p)
     return out
 
 
@@ -567,10 +571,10 @@ def moe_gather_mx4(hidden: torch.Tensor, k: int, inv_perm: torch.Tensor, capacit
     Rows of no slot are left as they were."""
     T, H = _matrix(hidden, "hidden")
     dev = hidden.get_device()
-    out = _mx4_out(out, capacity, H, hidden.device)
+    out, codes, scales = _mx4_out(out, capacity, H, hidden)
     _call("moe_gather_mx4", dev, stream, _arg(hidden, "hidden", torch.bfloat16, (T, H), dev), T, H, k,
           _arg(inv_perm, "inv_perm", torch.int32, (T * k,), dev), capacity,
-          *_mx4_args(out, "out.codes", "out.scales", dev), _status_arg(device_status, dev))
+          codes, scales, _status_arg(device_status, dev))
     return out
 
 
@@ -590,11 +594,9 @@ def moe_grouped_gemm_mx4(x: Mx4Tensor, w: Mx4Tensor, counts: torch.Tensor, offse
     if swiglu and N % 2 != 0:
         raise ValueError(f"swiglu needs an even number of features, got {N}")
     cols = N // 2 if swiglu else N
-    if out is None:
-        out = torch.empty((capacity, cols), dtype=torch.bfloat16, device=x.codes.device)
+    out, p = _out(out, "out", torch.bfloat16, (capacity, cols), x.codes)
     _call("moe_grouped_gemm_mx4", dev, stream, *_mx4_args(x, "x.codes", "x.scales", dev),
           *_mx4_args(w, "w.codes", "w.scales", dev),
           _arg(counts, "counts", torch.int32, (E,), dev), _arg(offsets, "offsets", torch.int32, (E + 1,), dev), E,
-          capacity, N, K, MOE_MX4_SWIGLU if swiglu else 0, _arg(out, "out", torch.bfloat16, (capacity, cols), dev),
-          _status_arg(device_status, dev))
+          capacity, N, K, MOE_MX4_SWIGLU if swiglu else 0, p, _status_arg(device_status, dev))
     return out
