@@ -525,12 +525,6 @@ def alloc_mx4(rows: int, K: int, device) -> Mx4Tensor:
                      torch.empty((-(-K // 128), rows, 4), dtype=torch.uint8, device=device))
 
 
-def _mx4_args(q: Mx4Tensor, codes_name: str, scales_name: str, index: int):
-    rows, half = _matrix(q.codes, codes_name)
-    return (_arg(q.codes, codes_name, torch.uint8, (rows, half), index),
-            _arg(q.scales, scales_name, torch.uint8, ((half + 63) // 64, rows, 4), index))
-
-
 def _mx4_out(out: Optional[Mx4Tensor], rows: int, K: int, like: torch.Tensor):
     """An output in the format and its addresses: `out`, checked, or a new one on `like`'s device."""
     if out is None:
@@ -539,9 +533,9 @@ def _mx4_out(out: Optional[Mx4Tensor], rows: int, K: int, like: torch.Tensor):
         out = Mx4Tensor(like.new_empty((rows, K // 2), dtype=torch.uint8),
                         like.new_empty((-(-K // 128), rows, 4), dtype=torch.uint8))
         return out, out.codes.data_ptr(), out.scales.data_ptr()
-    if (out.rows, out.K) != (rows, K):
-        raise ValueError(f"out holds [{out.rows}, {out.K}], [{rows}, {K}] is needed")
-    return (out, *_mx4_args(out, "out.codes", "out.scales", like.get_device()))
+    index = like.get_device()
+    return (out, _arg(out[0], "out.codes", torch.uint8, (rows, K // 2), index),
+            _arg(out[1], "out.scales", torch.uint8, ((K + 127) // 128, rows, 4), index))
 
 
 def moe_quantize_mx4(x: torch.Tensor, out: Optional[Mx4Tensor] = None, num_rows: Optional[torch.Tensor] = None,
@@ -558,9 +552,11 @@ def moe_quantize_mx4(x: torch.Tensor, out: Optional[Mx4Tensor] = None, num_rows:
 
 def moe_dequantize_mx4(q: Mx4Tensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The values of q as bf16 [rows, K]."""
-    dev, (rows, half) = q.codes.get_device(), _matrix(q.codes, "q.codes")
-    out, p = _out(out, "out", torch.bfloat16, (rows, 2 * half), q.codes)
-    _call("moe_dequantize_mx4", dev, stream, *_mx4_args(q, "q.codes", "q.scales", dev), rows, 2 * half, p)
+    codes, scales = q
+    dev, (rows, half) = codes.get_device(), _matrix(codes, "q.codes")
+    out, p = _out(out, "out", torch.bfloat16, (rows, 2 * half), codes)
+    _call("moe_dequantize_mx4", dev, stream, _arg(codes, "q.codes", torch.uint8, (rows, half), dev),
+          _arg(scales, "q.scales", torch.uint8, ((half + 63) // 64, rows, 4), dev), rows, 2 * half, p)
     return out
 
 
@@ -584,19 +580,20 @@ def moe_grouped_gemm_mx4(x: Mx4Tensor, w: Mx4Tensor, counts: torch.Tensor, offse
     """The experts' product on expert-grouped rows: x [capacity, K], w [E_local * N, K] (expert e's feature n in row
     e * N + n), counts [E_local] and offsets [E_local + 1] as from moe_align_permute -> out [capacity, N] bf16, or
     [capacity, N/2] = silu(first half) * second half with swiglu.  Rows of no expert are left as they were."""
-    dev = x.codes.get_device()
-    E, capacity, K, w_rows = counts.numel(), x.rows, x.K, w.rows
+    (xc, xs), (wc, ws), u8 = x, w, torch.uint8
+    dev, E = xc.get_device(), counts.numel()
+    (capacity, half), (w_rows, w_half) = _matrix(xc, "x.codes"), _matrix(wc, "w.codes")
     if E < 1 or w_rows % E != 0:
         raise ValueError(f"w must hold E_local * N rows, got {w_rows} for {E} experts")
-    if w.K != K:
-        raise ValueError(f"x has rows of {K}, w of {w.K}")
-    N = w_rows // E
+    if w_half != half:
+        raise ValueError(f"x has rows of {2 * half}, w of {2 * w_half}")
+    N, chunks = w_rows // E, (half + 63) // 64
     if swiglu and N % 2 != 0:
         raise ValueError(f"swiglu needs an even number of features, got {N}")
-    cols = N // 2 if swiglu else N
-    out, p = _out(out, "out", torch.bfloat16, (capacity, cols), x.codes)
-    _call("moe_grouped_gemm_mx4", dev, stream, *_mx4_args(x, "x.codes", "x.scales", dev),
-          *_mx4_args(w, "w.codes", "w.scales", dev),
-          _arg(counts, "counts", torch.int32, (E,), dev), _arg(offsets, "offsets", torch.int32, (E + 1,), dev), E,
-          capacity, N, K, MOE_MX4_SWIGLU if swiglu else 0, p, _status_arg(device_status, dev))
+    out, p = _out(out, "out", torch.bfloat16, (capacity, N // 2 if swiglu else N), xc)
+    _call("moe_grouped_gemm_mx4", dev, stream, _arg(xc, "x.codes", u8, (capacity, half), dev),
+          _arg(xs, "x.scales", u8, (chunks, capacity, 4), dev), _arg(wc, "w.codes", u8, (w_rows, half), dev),
+          _arg(ws, "w.scales", u8, (chunks, w_rows, 4), dev), _arg(counts, "counts", torch.int32, (E,), dev),
+          _arg(offsets, "offsets", torch.int32, (E + 1,), dev), E, capacity, N, 2 * half,
+          MOE_MX4_SWIGLU if swiglu else 0, p, _status_arg(device_status, dev))
     return out

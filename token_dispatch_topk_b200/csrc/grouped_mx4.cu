@@ -78,7 +78,6 @@ struct ProductArgs {
   const int32_t* counts;
   const int32_t* offsets;
   int E, N, K;
-  int chunks;     // ceil(K / 128)
   int kstages;    // ceil(K / 256)
   int ftiles;     // feature tiles (of a CTA, or of a pair)
   int gate_box;   // 1: map_w has the gate's boxes (N a multiple of 32), 0: boxes of 16 rows
@@ -219,9 +218,10 @@ __device__ __forceinline__ void stmatrix_trans(uint32_t addr, uint32_t a, uint32
                : "memory");
 }
 
+// silu(g) u, with the exponential taken of -|g|: the divisor stays between 1 and 2 (__fdividef gives 0 beyond 2^126).
 __device__ __forceinline__ float silu_times(uint32_t gate, uint32_t up) {
-  const float g = __uint_as_float(gate);
-  return __fdividef(g, 1.f + __expf(-g)) * __uint_as_float(up);
+  const float g = __uint_as_float(gate), t = __expf(-fabsf(g));
+  return __fdividef(g >= 0.f ? g : g * t, 1.f + t) * __uint_as_float(up);
 }
 
 // A bounded wait of a warp; it also gives up when another role of the CTA has.  The first test is inline and its vote
@@ -757,7 +757,12 @@ bool out_map(CUtensorMap* m, void* out, int64_t rows, int64_t cols, bool gate) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr int kPairRows = 64;  // rows an expert from which on pairs of CTAs take a tile
+// Rows of capacity an expert from which on pairs of CTAs take a tile.  Both forms with 128 experts and blocks of 16, us,
+// single | pair: 4096 -> 2816 gated, 8 rows an expert 127 | 132, 48 rows 132 | 138, 64 rows 161 | 139, 128 rows
+// 266 | 151; 768 -> 2048, 8 rows 22.6 | 23.9, 48 rows 25.4 | 26.3, 64 rows 31.9 | 27.4, 128 rows 50.8 | 32.1; one token of
+// six experts 4.7 | 5.7.  (A single CTA's tile ends at 64 rows.  The host knows the capacity, rows and padding; where
+// padding makes the most of it, 2 rows in blocks of 128, the pair costs 0 to 5 %.)
+constexpr int kPairRows = 64;
 
 template <int CG, bool kGate>
 moe_status_t launch_product(ProductArgs a, const CUtensorMap (&mx)[4], const CUtensorMap& mw,
@@ -788,7 +793,9 @@ moe_status_t launch_product(ProductArgs a, const CUtensorMap (&mx)[4], const CUt
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = CG == 1 ? 1 : 2;
-  return cudaLaunchKernelEx(&cfg, grouped_mx4_kernel<CG, kGate>, mx[0], mx[1], mx[2], mx[3], mw, mo, a) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, grouped_mx4_kernel<CG, kGate>, mx[0], mx[1], mx[2], mx[3], mw, mo, a) == cudaSuccess
+             ? MOE_OK
+             : MOE_ERR_CUDA;
 }
 
 }  // namespace
@@ -818,7 +825,6 @@ extern "C" moe_status_t moe_grouped_gemm_mx4(const void* x_codes, const void* x_
   a.E = E_local;
   a.N = N;
   a.K = K;
-  a.chunks = (K + 127) / 128;
   a.kstages = (K + kStageK - 1) / kStageK;
   a.ld_out = gate ? N / 2 : N;
   a.capacity = capacity;

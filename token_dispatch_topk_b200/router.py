@@ -77,7 +77,8 @@ class MoeRouter:
     def combine_backward(self, grad_out: torch.Tensor, expert_out: torch.Tensor,
                          topk_weights: Optional[torch.Tensor] = None, stream=None):
         """The combine's gradients for the step's routes: (grad_expert_out, grad_topk_weights), both this router's
-        buffers.  The pad rows of grad_expert_out below N_pad are +0, so products over whole blocks may use it."""
+        buffers.  The pad rows of grad_expert_out below N_pad are +0, so products over whole blocks may use it.
+        Under expert parallelism the weights' gradient of a remote slot is 0 here: sum it over the ranks."""
         self._needs_training()
         w = self.topk_weights if topk_weights is None else topk_weights
         return B.moe_combine_backward(grad_out, expert_out, w, self.align.inv_perm, self.grad_expert_out,
