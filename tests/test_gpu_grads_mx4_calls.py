@@ -199,3 +199,23 @@ def test_no_tokens():
     out = torch.full((5, 8), 7.0, dtype=BF16, device=dev)
     tdt.moe_grouped_gemm_mx4(q, wq, torch.zeros(1, dtype=I32, device=dev), torch.zeros(2, dtype=I32, device=dev), out)
     assert (out == 7).all()
+
+
+@pytest.mark.parametrize("as_handle", [False, True])
+def test_new_outputs_do_not_take_memory_in_use_on_another_stream(as_handle):
+    """A tensor freed while the current stream still has to read it is not handed to a call on a side stream."""
+    require_gpu()
+    rows, K = 4096, 2048
+    q = tdt.moe_quantize_mx4(torch.full((rows, K), 3.0, dtype=BF16, device="cuda"))
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    x = torch.full((rows, K), 5.0, dtype=BF16, device="cuda")
+    y = torch.empty_like(x)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)  # about 0.1 s
+    y.copy_(x)
+    del x
+    back = tdt.moe_dequantize_mx4(q, stream=side.cuda_stream if as_handle else side)
+    torch.cuda.synchronize()
+    assert (y == 5).all() and (back == 3).all()

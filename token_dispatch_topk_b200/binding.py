@@ -395,10 +395,21 @@ def _arg(t, name: str, dtype, shape, index: int) -> int:
     raise ValueError(f"{name} must be contiguous")
 
 
-def _out(t, name: str, dtype, shape, like: torch.Tensor):
-    """An output and its address: t, checked, or a new tensor on `like`'s device."""
+def _new(like: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
+    """A new tensor on `like`'s device, from the memory of the stream that will write it: memory freed on another stream
+    may still be in use there."""
+    if stream is None or not like.is_cuda:
+        return like.new_empty(shape, dtype=dtype)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=like.device)
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
+
+
+def _out(t, name: str, dtype, shape, like: torch.Tensor, stream):
+    """An output and its address: t, checked, or a new tensor."""
     if t is None:
-        t = like.new_empty(shape, dtype=dtype)
+        t = _new(like, shape, dtype, stream)
         return t, t.data_ptr()
     return t, _arg(t, name, dtype, shape, like.get_device())
 
@@ -453,8 +464,8 @@ def moe_combine_backward(grad_out: torch.Tensor, expert_out: torch.Tensor, topk_
     k = _matrix(topk_weights, "topk_weights")[1]
     capacity = _matrix(expert_out, "expert_out")[0]
     dev, bf16 = grad_out.get_device(), torch.bfloat16
-    grad_expert_out, gy = _out(grad_expert_out, "grad_expert_out", bf16, (capacity, H), grad_out)
-    grad_topk_weights, gw = _out(grad_topk_weights, "grad_topk_weights", torch.float32, (T, k), grad_out)
+    grad_expert_out, gy = _out(grad_expert_out, "grad_expert_out", bf16, (capacity, H), grad_out, stream)
+    grad_topk_weights, gw = _out(grad_topk_weights, "grad_topk_weights", torch.float32, (T, k), grad_out, stream)
     pads = (None, None)
     if zero_pad:
         pads = (_arg(sorted_token_ids, "sorted_token_ids", torch.int32, (capacity,), dev),
@@ -476,7 +487,7 @@ def moe_gather_backward(grad_permuted: torch.Tensor, inv_perm: torch.Tensor, k: 
     if k < 1 or inv_perm.numel() % k != 0:
         raise ValueError(f"inv_perm must hold T * k slots, got {inv_perm.numel()} with k = {k}")
     T, dev = inv_perm.numel() // k, grad_permuted.get_device()
-    grad_hidden, gx = _out(grad_hidden, "grad_hidden", torch.bfloat16, (T, H), grad_permuted)
+    grad_hidden, gx = _out(grad_hidden, "grad_hidden", torch.bfloat16, (T, H), grad_permuted, stream)
     _call("moe_gather_backward", dev, stream,
           _arg(grad_permuted, "grad_permuted", torch.bfloat16, (capacity, H), dev),
           _arg(inv_perm, "inv_perm", torch.int32, (T * k,), dev), T, k, H, capacity, gx, _status_arg(device_status, dev))
@@ -494,7 +505,7 @@ def moe_topk_softmax_backward(grad_topk_weights: torch.Tensor, logits: torch.Ten
     dev, dtype = logits.get_device(), logits.dtype
     if dtype not in (torch.bfloat16, torch.float32):
         raise ValueError(f"logits dtype {dtype} unsupported (bf16 or fp32)")
-    grad_logits, gx = _out(grad_logits, "grad_logits", dtype, (T, E), logits)
+    grad_logits, gx = _out(grad_logits, "grad_logits", dtype, (T, E), logits, stream)
     f32 = torch.float32
     _call("moe_topk_softmax_backward", dev, stream, _arg(grad_topk_weights, "grad_topk_weights", f32, (T, k), dev),
           _arg(logits, "logits", dtype, (T, E), dev), MOE_DTYPE_BF16 if dtype == torch.bfloat16 else MOE_DTYPE_F32,
@@ -525,13 +536,13 @@ def alloc_mx4(rows: int, K: int, device) -> Mx4Tensor:
                      torch.empty((-(-K // 128), rows, 4), dtype=torch.uint8, device=device))
 
 
-def _mx4_out(out: Optional[Mx4Tensor], rows: int, K: int, like: torch.Tensor):
-    """An output in the format and its addresses: `out`, checked, or a new one on `like`'s device."""
+def _mx4_out(out: Optional[Mx4Tensor], rows: int, K: int, like: torch.Tensor, stream):
+    """An output in the format and its addresses: `out`, checked, or a new one."""
     if out is None:
         if K < 32 or K % 32 != 0:
             raise ValueError(f"a row holds whole blocks of 32 elements, got K = {K}")
-        out = Mx4Tensor(like.new_empty((rows, K // 2), dtype=torch.uint8),
-                        like.new_empty((-(-K // 128), rows, 4), dtype=torch.uint8))
+        out = Mx4Tensor(_new(like, (rows, K // 2), torch.uint8, stream),
+                        _new(like, (-(-K // 128), rows, 4), torch.uint8, stream))
         return out, out.codes.data_ptr(), out.scales.data_ptr()
     index = like.get_device()
     return (out, _arg(out[0], "out.codes", torch.uint8, (rows, K // 2), index),
@@ -543,7 +554,7 @@ def moe_quantize_mx4(x: torch.Tensor, out: Optional[Mx4Tensor] = None, num_rows:
     """x [rows, K] bf16 -> microscaled 4-bit floating point (K a multiple of 32).  num_rows (int32 [1] on the device):
     rows from there on are neither read nor written."""
     rows, K = _matrix(x, "x")
-    out, codes, scales = _mx4_out(out, rows, K, x)
+    out, codes, scales = _mx4_out(out, rows, K, x, stream)
     dev = x.get_device()
     _call("moe_quantize_mx4", dev, stream, _arg(x, "x", torch.bfloat16, (rows, K), dev), rows, K,
           None if num_rows is None else _arg(num_rows, "num_rows", torch.int32, (1,), dev), codes, scales)
@@ -554,7 +565,7 @@ def moe_dequantize_mx4(q: Mx4Tensor, out: Optional[torch.Tensor] = None, stream=
     """The values of q as bf16 [rows, K]."""
     codes, scales = q
     dev, (rows, half) = codes.get_device(), _matrix(codes, "q.codes")
-    out, p = _out(out, "out", torch.bfloat16, (rows, 2 * half), codes)
+    out, p = _out(out, "out", torch.bfloat16, (rows, 2 * half), codes, stream)
     _call("moe_dequantize_mx4", dev, stream, _arg(codes, "q.codes", torch.uint8, (rows, half), dev),
           _arg(scales, "q.scales", torch.uint8, ((half + 63) // 64, rows, 4), dev), rows, 2 * half, p)
     return out
@@ -567,7 +578,7 @@ def moe_gather_mx4(hidden: torch.Tensor, k: int, inv_perm: torch.Tensor, capacit
     Rows of no slot are left as they were."""
     T, H = _matrix(hidden, "hidden")
     dev = hidden.get_device()
-    out, codes, scales = _mx4_out(out, capacity, H, hidden)
+    out, codes, scales = _mx4_out(out, capacity, H, hidden, stream)
     _call("moe_gather_mx4", dev, stream, _arg(hidden, "hidden", torch.bfloat16, (T, H), dev), T, H, k,
           _arg(inv_perm, "inv_perm", torch.int32, (T * k,), dev), capacity,
           codes, scales, _status_arg(device_status, dev))
@@ -590,7 +601,7 @@ def moe_grouped_gemm_mx4(x: Mx4Tensor, w: Mx4Tensor, counts: torch.Tensor, offse
     N, chunks = w_rows // E, (half + 63) // 64
     if swiglu and N % 2 != 0:
         raise ValueError(f"swiglu needs an even number of features, got {N}")
-    out, p = _out(out, "out", torch.bfloat16, (capacity, N // 2 if swiglu else N), xc)
+    out, p = _out(out, "out", torch.bfloat16, (capacity, N // 2 if swiglu else N), xc, stream)
     _call("moe_grouped_gemm_mx4", dev, stream, _arg(xc, "x.codes", u8, (capacity, half), dev),
           _arg(xs, "x.scales", u8, (chunks, capacity, 4), dev), _arg(wc, "w.codes", u8, (w_rows, half), dev),
           _arg(ws, "w.scales", u8, (chunks, w_rows, 4), dev), _arg(counts, "counts", torch.int32, (E,), dev),
