@@ -42,26 +42,26 @@ struct CombineGradArgs {
   const int32_t* sorted_ids;  // pads: null unless the pad rows are to be zeroed
   const int32_t* n_pad;
   int64_t slot_blocks;      // CTAs below this index take slots, the others pad rows
+  int pad_rows;             // rows that a warp of those looks at, up to 32
   int32_t* status;
 };
 
-constexpr int kPadRowsPerCta = kWarps * 32;
 
 // One warp per slot; the k slots of a token sit in neighbouring warps, so its gradient row comes from DRAM once
 // and from L1 / L2 after that.  Bandwidth-bound: a row of y in, a row of gy out, 16 bytes a lane and kUnroll
 // vectors in flight.
 __global__ void __launch_bounds__(kWarps * 32) combine_grad_kernel(CombineGradArgs a) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   moe::pdl_launch_dependents();
   moe::pdl_wait();  // every input may come from the previous kernel
   if (blockIdx.x >= a.slot_blocks) {  // +0 into the pad rows below N_pad (their sorted id is T*k)
-    const int64_t p0 = (static_cast<int64_t>(blockIdx.x) - a.slot_blocks) * kPadRowsPerCta;
+    const int64_t p0 = ((static_cast<int64_t>(blockIdx.x) - a.slot_blocks) * kWarps + warp) * a.pad_rows;
     int64_t end = a.n_pad[0];
     if (end > a.capacity) end = a.capacity;
-    const int64_t p = p0 + tid;  // a lane looks at a row, the warp then writes its pad rows one by one
-    unsigned pads = __ballot_sync(0xffffffffu, p < end && a.sorted_ids[p] == static_cast<int32_t>(a.slots));
-    for (; pads != 0u; pads &= pads - 1u) {
-      uint4* row = a.gy + (p0 + warp * 32 + __ffs(pads) - 1) * a.nv;
+    // a lane looks at a row, the warp then writes its pad rows one by one
+    const bool pad = lane < a.pad_rows && p0 + lane < end && a.sorted_ids[p0 + lane] == static_cast<int32_t>(a.slots);
+    for (unsigned pads = __ballot_sync(0xffffffffu, pad); pads != 0u; pads &= pads - 1u) {
+      uint4* row = a.gy + (p0 + __ffs(pads) - 1) * a.nv;
       for (int v = lane; v < a.nv; v += 32) moe::st_plain(row + v, make_uint4(0u, 0u, 0u, 0u));
     }
     return;
@@ -468,7 +468,14 @@ extern "C" moe_status_t moe_combine_backward(const void* grad_out, const void* e
   a.n_pad = num_tokens_post_pad;
   a.slot_blocks = (a.slots + kWarps - 1) / kWarps;
   a.status = device_status;
-  const int64_t grid = a.slot_blocks + (zero_pad ? (capacity + kPadRowsPerCta - 1) / kPadRowsPerCta : 0);
+  int64_t grid = a.slot_blocks;
+  if (zero_pad) {  // a few rows a warp where there are few (mostly pads in a small batch), so that all SMs write
+    const int sms = moe_host::sm_count();
+    if (sms <= 0) return MOE_ERR_CUDA;
+    const int64_t rows = capacity / (int64_t{16} * sms);
+    a.pad_rows = rows < 1 ? 1 : rows > 32 ? 32 : static_cast<int>(rows);
+    grid += (capacity + kWarps * a.pad_rows - 1) / (kWarps * a.pad_rows);
+  }
   return moe_host::launch_pdl(combine_grad_kernel, dim3(static_cast<unsigned>(grid)), dim3(kWarps * 32), 0,
                               static_cast<cudaStream_t>(stream), a);
 }
