@@ -363,7 +363,8 @@ MOE_API moe_status_t moe_gather_backward(const void* grad_permuted, const int32_
  *   dtype: of logits and grad_logits [T, E]; topk_weights and topk_ids as moe_topk_softmax returned them with the same
  *   flags.  Computed in fp32, one rounding to dtype.  The gradients of an expert named twice in a row add up.  An id
  *   outside [0, E) is left out and MOE_ERR_BAD_EXPERT_ID recorded in device_status (a device int32 or NULL).
- *   grad_logits may be logits itself.  Errors: as for moe_topk_softmax.
+ *   grad_logits may be logits itself.  Preconditions: finite logits; -infinity (a masked expert) is allowed where a row
+ *   has a finite logit, and gets a gradient of 0 unless it was selected.  Errors: as for moe_topk_softmax.
  */
 MOE_API moe_status_t moe_topk_softmax_backward(const float* grad_topk_weights, const void* logits,
                                                moe_dtype_t dtype, const float* topk_weights,

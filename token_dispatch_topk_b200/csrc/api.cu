@@ -18,7 +18,7 @@ extern "C" const char* moe_status_string(moe_status_t status) {
   }
 }
 
-extern "C" int32_t moe_version(void) { return 100; /* 0.1.0 */ }
+extern "C" int32_t moe_version(void) { return 200; /* 0.2.0 */ }
 
 extern "C" moe_status_t moe_workspace_init(void* workspace, size_t bytes, void* stream) {
   if (workspace == nullptr && bytes > 0) return MOE_ERR_INVALID_ARG;

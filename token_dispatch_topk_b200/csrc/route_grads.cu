@@ -190,7 +190,6 @@ gather_grad_kernel(const uint4* __restrict__ gp, const int32_t* __restrict__ inv
 
 // ---------------------------------------------------------------------------------------------- gating --
 constexpr int kGateWarps = 8;
-constexpr int kGateFloats = 1024;  // of shared memory a warp: the most experts of its 32 / G rows (G lanes a row)
 
 struct GateGradArgs {
   const float* gw;      // [T, k] incoming
@@ -202,6 +201,7 @@ struct GateGradArgs {
   int renorm, sigmoid;
   int kp_log2;          // log2 of the lanes a row's slots take (k rounded up to a power of two)
   int g_log2;           // log2 of the lanes a row's logits take (dense)
+  int sums;             // floats of shared memory a warp's rows take (dense; a multiple of 4)
   void* gx;             // [T, E] out
   int32_t* status;
 };
@@ -335,10 +335,10 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_grad_sparse_kernel(GateG
 // recomputed.
 template <typename TX, int VEC, int CPL>
 __global__ void __launch_bounds__(kGateWarps * 32) gate_grad_dense_kernel(GateGradArgs a) {
-  __shared__ __align__(16) float s_rows[kGateWarps][kGateFloats];
+  extern __shared__ __align__(16) float s_rows[];  // as much as the rows need: more would cost resident warps
   __shared__ float s_sum[kGateWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.E;
-  float* sums = s_rows[warp];
+  float* sums = s_rows + warp * a.sums;
   const int G = 1 << a.g_log2, rows = 32 >> a.g_log2, l = lane & (G - 1), r = lane >> a.g_log2, chunks = E / VEC;
   const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kGateWarps + warp) * rows;
   const int n = a.T - t0 < rows ? static_cast<int>(a.T - t0) : rows;
@@ -429,9 +429,11 @@ moe_status_t launch_gate_grad(GateGradArgs a, cudaStream_t st) {
     kernel = wide ? dense_kernel<TX, kWide>(cpl) : dense_kernel<TX, 1>(cpl);
   else
     kernel = wide ? gate_grad_sparse_kernel<TX, kWide> : gate_grad_sparse_kernel<TX, 1>;
+  a.sums = (rows * a.E + 3) & ~3;  // at most 1024 where dense: one row of up to 1024, or 32 / G of up to 8 G elements
+  const size_t smem = dense ? kGateWarps * a.sums * sizeof(float) : 0;
   const int64_t batches = (a.T + rows - 1) / rows;
   return moe_host::launch_pdl(kernel, dim3(static_cast<unsigned>((batches + kGateWarps - 1) / kGateWarps)),
-                              dim3(kGateWarps * 32), 0, st, a);
+                              dim3(kGateWarps * 32), smem, st, a);
 }
 
 }  // namespace
