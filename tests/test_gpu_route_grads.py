@@ -209,6 +209,20 @@ def test_gating_backward(T, E, k, dtype, scoring, renorm):
     assert torch.equal(inplace, gx)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,E,k", [(151001, 8, 2), (20003, 60, 4), (40001, 256, 8), (30011, 34, 1), (10007, 130, 32)])
+def test_gating_backward_large_batches(T, E, k, dtype):
+    """The softmax over all experts where a warp takes several groups of rows, and a ragged last warp."""
+    require_gpu()
+    x = torch.randn((T, E), generator=torch.Generator("cuda").manual_seed(E), device="cuda").to(dtype)
+    w, ids = tdt.moe_topk_softmax(x, k, False)
+    g = torch.randn((T, k), generator=torch.Generator("cuda").manual_seed(k), device="cuda")
+    gx = tdt.moe_topk_softmax_backward(g, x, w, ids, False)
+    want = gate_reference(g, x, w, ids, False, "softmax")
+    tol = gate_tolerance(g, x, w, ids, False, "softmax")
+    within(gx, want, tol * (1 + 2.0 ** -7) + want.abs() * HALF[dtype] + TINY, "grad_logits")
+
+
 @pytest.mark.parametrize("renorm", [True, False])
 @pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
 def test_gating_backward_against_differences(scoring, renorm):

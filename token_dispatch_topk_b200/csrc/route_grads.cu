@@ -201,6 +201,7 @@ struct GateGradArgs {
   int renorm, sigmoid;
   int kp_log2;          // log2 of the lanes a row's slots take (k rounded up to a power of two)
   int g_log2;           // log2 of the lanes a row's logits take (dense)
+  int iters;            // groups of 32 / G rows a warp takes (dense)
   int sums;             // floats of shared memory a warp's rows take (dense; a multiple of 4)
   void* gx;             // [T, E] out
   int32_t* status;
@@ -330,16 +331,21 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_grad_sparse_kernel(GateG
   }
 }
 
-// The softmax over all experts: every logit has a gradient.  A row takes G lanes, CPL vectors each, read once and first
-// of all; the selected experts' g_j go into the row's fp32 sums in shared memory meanwhile; the probabilities are
-// recomputed.
-template <typename TX, int VEC, int CPL>
-__global__ void __launch_bounds__(kGateWarps * 32) gate_grad_dense_kernel(GateGradArgs a) {
+// The softmax over all experts: every logit has a gradient.  A row takes G lanes, CPL vectors each; a warp takes
+// a.iters (at most R, and R CPL VEC <= 32 registers) times 32 / G rows, all read first of all; the selected experts' g_j
+// go into the rows' fp32 sums in shared memory meanwhile; the probabilities are recomputed.  Small batches wait for two
+// dependent loads (16384 x 60 fp32: 4.5 us, 5.9 with one group of rows a warp), large ones for the chain of shuffles and
+// exponentials of a row (65536 x 256 bf16: 37 us, 48 with one group, against 11 at the copy rate).  At most 64 registers:
+// 37 us against 40.
+constexpr int kDenseRows = 64;  // of a warp, at most
+template <typename TX, int VEC, int CPL, int R>
+__global__ void __launch_bounds__(kGateWarps * 32, 4) gate_grad_dense_kernel(GateGradArgs a) {
   extern __shared__ __align__(16) float s_rows[];  // as much as the rows need: more would cost resident warps
-  __shared__ float s_sum[kGateWarps][32];
+  __shared__ float s_sum[kGateWarps][kDenseRows];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.E;
   float* sums = s_rows + warp * a.sums;
-  const int G = 1 << a.g_log2, rows = 32 >> a.g_log2, l = lane & (G - 1), r = lane >> a.g_log2, chunks = E / VEC;
+  const int G = 1 << a.g_log2, side = 32 >> a.g_log2, rows = side * a.iters;
+  const int l = lane & (G - 1), r1 = lane >> a.g_log2, chunks = E / VEC;
   const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kGateWarps + warp) * rows;
   const int n = a.T - t0 < rows ? static_cast<int>(a.T - t0) : rows;
   for (int i = lane * 4; i < n * E; i += 128) *reinterpret_cast<float4*>(sums + i) = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -348,13 +354,17 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_grad_dense_kernel(GateGr
   if (n <= 0) return;  // uniform per warp
   const TX* x = static_cast<const TX*>(a.x) + t0 * E;
   TX* gx = static_cast<TX*>(a.gx) + t0 * E;
-  float v[CPL][VEC];
+  float v[R][CPL][VEC];
 #pragma unroll
-  for (int i = 0; i < CPL; ++i) {
-    const int c = l + i * G;
+  for (int o = 0; o < R; ++o) {
+    const int r = o * side + r1;
 #pragma unroll
-    for (int q = 0; q < VEC; ++q) v[i][q] = -INFINITY;
-    if (r < n && c < chunks) RowVec<TX, VEC>::load(x + r * E + c * VEC, v[i]);
+    for (int i = 0; i < CPL; ++i) {
+      const int c = l + i * G;
+#pragma unroll
+      for (int q = 0; q < VEC; ++q) v[o][i][q] = -INFINITY;
+      if (r < n && c < chunks) RowVec<TX, VEC>::load(x + r * E + c * VEC, v[o][i]);
+    }
   }
   __syncwarp();
   for (int r0 = 0; r0 < n; r0 += 32 >> a.kp_log2) {
@@ -363,32 +373,37 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_grad_dense_kernel(GateGr
     if (s.lead) sums[rs * E + s.id] = s.value;
     if ((lane & ((1 << a.kp_log2) - 1)) == 0 && rs < n) s_sum[warp][rs] = s.G;
   }
-  float m = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < CPL; ++i)
-#pragma unroll
-    for (int q = 0; q < VEC; ++q) m = fmaxf(m, v[i][q]);
-  for (int d = G >> 1; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-  float z = 0.f;
-#pragma unroll
-  for (int i = 0; i < CPL; ++i)
-#pragma unroll
-    for (int q = 0; q < VEC; ++q) {
-      v[i][q] = expf(v[i][q] - m);
-      if (r < n && l + i * G < chunks) z += v[i][q];
-    }
-  for (int d = G >> 1; d > 0; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
-  z = 1.f / z;
   __syncwarp();
-  if (r < n) {
-    const float mean = s_sum[warp][r];
 #pragma unroll
-    for (int i = 0; i < CPL; ++i) {
-      const int c = l + i * G;
-      if (c < chunks) {
+  for (int o = 0; o < R; ++o) {
+    if (o >= a.iters) break;  // uniform
+    const int r = o * side + r1;
+    float m = -INFINITY;
 #pragma unroll
-        for (int q = 0; q < VEC; ++q) v[i][q] = v[i][q] * z * (sums[r * E + c * VEC + q] - mean);
-        RowVec<TX, VEC>::store(gx + r * E + c * VEC, v[i]);
+    for (int i = 0; i < CPL; ++i)
+#pragma unroll
+      for (int q = 0; q < VEC; ++q) m = fmaxf(m, v[o][i][q]);
+    for (int d = G >> 1; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    float z = 0.f;
+#pragma unroll
+    for (int i = 0; i < CPL; ++i)
+#pragma unroll
+      for (int q = 0; q < VEC; ++q) {
+        v[o][i][q] = expf(v[o][i][q] - m);
+        if (r < n && l + i * G < chunks) z += v[o][i][q];
+      }
+    for (int d = G >> 1; d > 0; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
+    z = 1.f / z;
+    if (r < n) {
+      const float mean = s_sum[warp][r];
+#pragma unroll
+      for (int i = 0; i < CPL; ++i) {
+        const int c = l + i * G;
+        if (c < chunks) {
+#pragma unroll
+          for (int q = 0; q < VEC; ++q) v[o][i][q] = v[o][i][q] * z * (sums[r * E + c * VEC + q] - mean);
+          RowVec<TX, VEC>::store(gx + r * E + c * VEC, v[o][i]);
+        }
       }
     }
   }
@@ -397,19 +412,24 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_grad_dense_kernel(GateGr
 using GateKernel = void (*)(GateGradArgs);
 
 // Vectors a lane for the dense gradient: the next of {1, 2, 4} (16-byte vectors of bf16), {1, 2, 8} (of fp32) or
-// {2, 8, 32} (single elements) that holds E experts.
+// {2, 8, 32} (single elements) that holds E experts; and the row groups a warp holds in 32 registers a lane, at most 4.
+struct DenseKernel {
+  GateKernel kernel;
+  int most;
+};
+template <typename TX, int VEC, int CPL>
+DenseKernel dense_kernel() {
+  constexpr int R = VEC * CPL >= 32 ? 1 : VEC * CPL >= 16 ? 2 : 4;
+  return {gate_grad_dense_kernel<TX, VEC, CPL, R>, R};
+}
 template <typename TX, int VEC>
-GateKernel dense_kernel(int cpl) {
-  if constexpr (VEC == 8) {
-    return cpl <= 1 ? gate_grad_dense_kernel<TX, 8, 1>
-                    : cpl <= 2 ? gate_grad_dense_kernel<TX, 8, 2> : gate_grad_dense_kernel<TX, 8, 4>;
-  } else if constexpr (VEC == 4) {
-    return cpl <= 1 ? gate_grad_dense_kernel<TX, 4, 1>
-                    : cpl <= 2 ? gate_grad_dense_kernel<TX, 4, 2> : gate_grad_dense_kernel<TX, 4, 8>;
-  } else {
-    return cpl <= 2 ? gate_grad_dense_kernel<TX, 1, 2>
-                    : cpl <= 8 ? gate_grad_dense_kernel<TX, 1, 8> : gate_grad_dense_kernel<TX, 1, 32>;
-  }
+DenseKernel dense_kernel_for(int cpl) {
+  if constexpr (VEC == 8)
+    return cpl <= 1 ? dense_kernel<TX, 8, 1>() : cpl <= 2 ? dense_kernel<TX, 8, 2>() : dense_kernel<TX, 8, 4>();
+  else if constexpr (VEC == 4)
+    return cpl <= 1 ? dense_kernel<TX, 4, 1>() : cpl <= 2 ? dense_kernel<TX, 4, 2>() : dense_kernel<TX, 4, 8>();
+  else
+    return cpl <= 2 ? dense_kernel<TX, 1, 2>() : cpl <= 8 ? dense_kernel<TX, 1, 8>() : dense_kernel<TX, 1, 32>();
 }
 
 template <typename TX>
@@ -423,13 +443,24 @@ moe_status_t launch_gate_grad(GateGradArgs a, cudaStream_t st) {
   a.g_log2 = 0;
   while ((1 << a.g_log2) < chunks && a.g_log2 < 5) ++a.g_log2;
   const int cpl = (chunks + 31) / 32;
-  const int rows = 32 >> (dense ? a.g_log2 : a.kp_log2);
+  int rows = 32 >> (dense ? a.g_log2 : a.kp_log2);
   GateKernel kernel;
-  if (dense)
-    kernel = wide ? dense_kernel<TX, kWide>(cpl) : dense_kernel<TX, 1>(cpl);
-  else
+  if (dense) {
+    const DenseKernel d = wide ? dense_kernel_for<TX, kWide>(cpl) : dense_kernel_for<TX, 1>(cpl);
+    kernel = d.kernel;
+    // row groups a warp: as many as its registers hold, where that leaves every SM 16 warps and the rows' slots fill
+    // the lanes at most twice
+    const int sms = moe_host::sm_count();
+    if (sms <= 0) return MOE_ERR_CUDA;
+    a.iters = 1;
+    while (a.iters < d.most && 2 * a.iters * rows <= (kDenseRows >> a.kp_log2) &&
+           a.T >= int64_t{2} * a.iters * rows * sms * 16)
+      a.iters *= 2;
+    rows *= a.iters;
+  } else {
     kernel = wide ? gate_grad_sparse_kernel<TX, kWide> : gate_grad_sparse_kernel<TX, 1>;
-  a.sums = (rows * a.E + 3) & ~3;  // at most 1024 where dense: one row of up to 1024, or 32 / G of up to 8 G elements
+  }
+  a.sums = (rows * a.E + 3) & ~3;  // where dense at most 1024: rows E <= 32 CPL VEC iters
   const size_t smem = dense ? kGateWarps * a.sums * sizeof(float) : 0;
   const int64_t batches = (a.T + rows - 1) / rows;
   return moe_host::launch_pdl(kernel, dim3(static_cast<unsigned>((batches + kGateWarps - 1) / kGateWarps)),
