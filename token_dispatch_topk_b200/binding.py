@@ -401,7 +401,9 @@ def _new(like: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
     if stream is None or not like.is_cuda:
         return like.new_empty(shape, dtype=dtype)
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=like.device)
+        # (ExternalStream takes handle 0, the default stream's, for "no handle": it would be some stream of torch's pool)
+        handle = int(stream)
+        stream = torch.cuda.ExternalStream(handle, device=like.device) if handle else torch.cuda.default_stream(like.device)
     with torch.cuda.stream(stream):
         return like.new_empty(shape, dtype=dtype)
 
