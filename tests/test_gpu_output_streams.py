@@ -26,11 +26,11 @@ def test_handle_0_takes_the_default_streams_memory():
             torch.cuda._sleep(200_000_000)  # about 0.1 s
             ys[-1].copy_(x)
             del x
-    used = set()
+    used, last = set(), torch.empty((rows, K), dtype=torch.bfloat16, device="cuda")
     for _ in range(40):  # more calls than torch keeps streams in its pool
         back = tdt.moe_dequantize_mx4(q, stream=0)
         used.add(back.data_ptr())
-        last = back.clone()
+        last.copy_(back)
         del back
     torch.cuda.synchronize()
     assert all((y == 5).all() for y in ys) and (last == 3).all()
