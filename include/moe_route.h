@@ -346,7 +346,7 @@ MOE_API moe_status_t moe_combine_backward(const void* grad_out, const void* expe
  * moe_gather_backward -- gradient of moe_gather: grad_hidden[t,h] = bf16_rne(sum over the local slots j of
  *   grad_permuted[inv_perm[t*k+j], h]), summed in fp32 in slot order from +0; +0 for a token with no local slot.
  *   grad_permuted [capacity, H] bf16 (pad rows are not read); grad_hidden [T, H] bf16.
- *   Errors: as for moe_combine, and UNSUPPORTED beyond 2^40 elements; device_status: as for moe_gather.
+ *   Errors: as for moe_combine, and UNSUPPORTED for T * H beyond 2^40; device_status: as for moe_gather.
  */
 MOE_API moe_status_t moe_gather_backward(const void* grad_permuted, const int32_t* inv_perm, int64_t T, int32_t k,
                                          int32_t H, int64_t capacity, void* grad_hidden, int32_t* device_status,
@@ -390,7 +390,7 @@ MOE_API moe_status_t moe_topk_softmax_backward(const float* grad_topk_weights, c
  *   scales [ceil(H/128), capacity, 4] becomes the quantised hidden row s / k, for every local slot s.  A token's row
  *   is read and quantised once, not at all without a local slot.  Other rows are left as they were.
  * Errors: INVALID_ARG (sizes, K or H % 32 != 0 or beyond 2^20, 2^31 rows, null or misaligned pointers), UNSUPPORTED
- *   (k > 32, more than 2^41 elements).  device_status: as for moe_gather.
+ *   (k > 32, a matrix of more than 2^41 elements).  device_status: as for moe_gather.
  */
 MOE_API moe_status_t moe_quantize_mx4(const void* x, int64_t rows, int32_t K, const int32_t* num_rows, void* codes,
                                       void* scales, void* stream);

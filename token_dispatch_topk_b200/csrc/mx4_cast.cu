@@ -217,15 +217,15 @@ dequantize_kernel(const uint32_t* __restrict__ codes, const uint8_t* __restrict_
     if (v < nv && row + 2 * u < rows) moe::st_stream(out + (row + 2 * u) * nv + v, dequantize8(q[u], byte[u]));
 }
 
-// Sizes of a matrix in the format: K in blocks of 32, and every element index below 2^47.
+// Sizes of a matrix in the format: K in blocks of 32.  Beyond kMaxElements a call is refused as unsupported.
+constexpr int64_t kMaxElements = int64_t{1} << 41;
 bool mx4_sizes_ok(int64_t rows, int32_t K) {
   return rows >= 0 && rows < (int64_t{1} << 31) && K >= 32 && (K % 32) == 0 && K <= (1 << 20);
 }
 
-bool cast_grid(int64_t warps, unsigned* grid) {
-  const int64_t blocks = (warps + kCastThreads / 32 - 1) / (kCastThreads / 32);
-  *grid = static_cast<unsigned>(blocks);
-  return blocks <= 0x7fffffff;
+// CTAs for as many warps: below 2^30, as a warp takes 1024 elements or the rest of a row, and rows stay below 2^31
+unsigned cast_grid(int64_t warps) {
+  return static_cast<unsigned>((warps + kCastThreads / 32 - 1) / (kCastThreads / 32));
 }
 
 }  // namespace
@@ -233,13 +233,13 @@ bool cast_grid(int64_t warps, unsigned* grid) {
 extern "C" moe_status_t moe_quantize_mx4(const void* x, int64_t rows, int32_t K, const int32_t* num_rows,
                                          void* codes, void* scales, void* stream) {
   if (!mx4_sizes_ok(rows, K)) return MOE_ERR_INVALID_ARG;
+  if (rows * K > kMaxElements) return MOE_ERR_UNSUPPORTED;
   if (rows == 0) return MOE_OK;
   if (x == nullptr || codes == nullptr || scales == nullptr) return MOE_ERR_INVALID_ARG;
   if (!moe_host::aligned16(x) || !moe_host::aligned16(codes) || !moe_host::aligned16(scales))
     return MOE_ERR_INVALID_ARG;
   const int nv = K / 8, chunks = (K + 127) / 128;
-  unsigned grid;
-  if (!cast_grid((rows + kRowsPerWarp - 1) / kRowsPerWarp * chunks, &grid)) return MOE_ERR_UNSUPPORTED;
+  const unsigned grid = cast_grid((rows + kRowsPerWarp - 1) / kRowsPerWarp * chunks);
   return moe_host::launch_pdl(quantize_kernel, dim3(grid), dim3(kCastThreads), 0, static_cast<cudaStream_t>(stream),
                               static_cast<const uint4*>(x), rows, num_rows, nv, chunks, static_cast<uint32_t*>(codes),
                               static_cast<uint32_t*>(scales));
@@ -248,13 +248,13 @@ extern "C" moe_status_t moe_quantize_mx4(const void* x, int64_t rows, int32_t K,
 extern "C" moe_status_t moe_dequantize_mx4(const void* codes, const void* scales, int64_t rows, int32_t K, void* out,
                                            void* stream) {
   if (!mx4_sizes_ok(rows, K)) return MOE_ERR_INVALID_ARG;
+  if (rows * K > kMaxElements) return MOE_ERR_UNSUPPORTED;
   if (rows == 0) return MOE_OK;
   if (out == nullptr || codes == nullptr || scales == nullptr) return MOE_ERR_INVALID_ARG;
   if (!moe_host::aligned16(out) || !moe_host::aligned16(codes) || !moe_host::aligned16(scales))
     return MOE_ERR_INVALID_ARG;
   const int nv = K / 8, chunks = (K + 127) / 128;
-  unsigned grid;
-  if (!cast_grid((rows + kRowsPerWarp - 1) / kRowsPerWarp * chunks, &grid)) return MOE_ERR_UNSUPPORTED;
+  const unsigned grid = cast_grid((rows + kRowsPerWarp - 1) / kRowsPerWarp * chunks);
   return moe_host::launch_pdl(dequantize_kernel, dim3(grid), dim3(kCastThreads), 0,
                               static_cast<cudaStream_t>(stream), static_cast<const uint32_t*>(codes),
                               static_cast<const uint8_t*>(scales), rows, nv, chunks, static_cast<uint4*>(out));
@@ -266,14 +266,14 @@ extern "C" moe_status_t moe_gather_mx4(const void* hidden, int64_t T, int32_t H,
   if (T < 0 || k < 1 || !mx4_sizes_ok(capacity, H)) return MOE_ERR_INVALID_ARG;
   if (k > 32) return MOE_ERR_UNSUPPORTED;
   if (T > (int64_t{1} << 40) || T * k >= (int64_t{1} << 30)) return MOE_ERR_INVALID_ARG;
+  if (T * H > kMaxElements || capacity * H > kMaxElements) return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;
   if (hidden == nullptr || inv_perm == nullptr) return MOE_ERR_INVALID_ARG;
   if (capacity > 0 && (codes == nullptr || scales == nullptr)) return MOE_ERR_INVALID_ARG;
   if (!moe_host::aligned16(hidden) || !moe_host::aligned16(codes) || !moe_host::aligned16(scales))
     return MOE_ERR_INVALID_ARG;
   const int nv = H / 8, segs = (nv + 32 * kPieces - 1) / (32 * kPieces);
-  unsigned grid;
-  if (!cast_grid(T * segs, &grid)) return MOE_ERR_UNSUPPORTED;
+  const unsigned grid = cast_grid(T * segs);
   return moe_host::launch_pdl(gather_mx4_kernel, dim3(grid), dim3(kCastThreads), 0, static_cast<cudaStream_t>(stream),
                               static_cast<const uint4*>(hidden), T, nv, segs, static_cast<int>(k), inv_perm, capacity,
                               static_cast<uint32_t*>(codes), static_cast<uint32_t*>(scales), device_status);

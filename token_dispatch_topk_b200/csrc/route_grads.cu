@@ -556,6 +556,7 @@ extern "C" moe_status_t moe_gather_backward(const void* grad_permuted, const int
   if ((H % 8) != 0) return MOE_ERR_INVALID_ARG;
   if (T > (int64_t{1} << 40) || T * k >= (int64_t{1} << 30) || capacity >= (int64_t{1} << 31))
     return MOE_ERR_INVALID_ARG;
+  if (T * H > (int64_t{1} << 40)) return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;
   if (inv_perm == nullptr || grad_hidden == nullptr || (capacity > 0 && grad_permuted == nullptr))
     return MOE_ERR_INVALID_ARG;
@@ -566,8 +567,7 @@ extern "C" moe_status_t moe_gather_backward(const void* grad_permuted, const int
   if (sms <= 0) return MOE_ERR_CUDA;
   int per = 1;
   while (per < 4 && 2 * per * k <= 32 && T * segs >= int64_t{2} * per * sms * 64) per *= 2;
-  const int64_t grid = ((T + per - 1) / per * segs + kWarps - 1) / kWarps;
-  if (grid > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
+  const int64_t grid = ((T + per - 1) / per * segs + kWarps - 1) / kWarps;  // (T segs <= T H / 512 + T: below 2^29)
   const auto kernel = per == 1 ? gather_grad_kernel<4, true> : gather_grad_kernel<2, false>;
   return moe_host::launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(kWarps * 32), 0,
                               static_cast<cudaStream_t>(stream), static_cast<const uint4*>(grad_permuted), inv_perm, T,
