@@ -161,6 +161,17 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
         : "memory");
 }
 
+// Arrive at this CTA's own barrier once the tensor operations issued so far are done, in a pair those of both CTAs.
+template <int CG>
+__device__ __forceinline__ void commit_own(uint64_t* bar) {
+  if constexpr (CG == 1)
+    commit<1>(bar);
+  else
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                     moe::smem_addr(bar))
+                 : "memory");
+}
+
 // Arrive at CTA 0's barrier of the pair.  What it announces is in shared memory or TMEM, which have one copy, and was
 // complete before (the stage's own barrier, tcgen05.wait), so the release need not reach beyond the CTA: with
 // .release.cluster an arrival also waits for the CTA's global stores, about 1300 cycles, and bounded the whole kernel.
@@ -467,8 +478,14 @@ grouped_mx4_kernel(const __grid_constant__ CUtensorMap map_x16, const __grid_con
         if (++st == kStages) { st = 0; ++round; }
       }
     }
-    if (*abort != 0) {  // never leave with loads in flight into this CTA's shared memory
-      for (int64_t q = issued > kStages ? issued - kStages : 0; q < issued; ++q)
+    // Never leave with an arrival on its way to this CTA's barriers.  The last stages' releases (in a pair they come from
+    // the other CTA's commits) are waited for by nobody else; how they stand to the accumulator's arrival, which the
+    // epilogue waits for, is not promised.
+    const int64_t last = issued > kStages ? issued - kStages : 0;
+    for (int64_t q = last; ok && q < issued; ++q)
+      ok = wait_warp(&s.empty[q % kStages], static_cast<uint32_t>(q / kStages) & 1u, abort, a.status);
+    if (*abort != 0) {  // nor with loads in flight into this CTA's shared memory
+      for (int64_t q = last; q < issued; ++q)
         moe::mbar_wait(&s.full[q % kStages], static_cast<uint32_t>(q / kStages) & 1u, 200000000ull);
     }
   } else if (warp == 1 && rank == 0) {
@@ -524,10 +541,13 @@ grouped_mx4_kernel(const __grid_constant__ CUtensorMap map_x16, const __grid_con
       }
       if (++buf == 2) { buf = 0; ++buf_round; }
     }
-    if (*abort != 0) {  // products in flight still read shared memory and write TMEM
-      if (elect_one()) commit<CG>(&s.drained);
+    if (before != 0) {  // products in flight still read shared memory and write TMEM
+      if (elect_one()) commit_own<CG>(&s.drained);
       __syncwarp();
       moe::mbar_wait(&s.drained, 0, 200000000ull);
+      // after a wait that ran out, the other CTA may no longer wait for the arrivals of the commits above: they get a
+      // millisecond, where they take well under a microsecond
+      if (CG == 2 && *abort != 0) __nanosleep(1000000);
     }
   } else if (warp == 1) {  // the pair's second CTA: tell the first that a stage is there
     Tiles<CG, kGate> tl(a, s.first_tile, s.tiles);
