@@ -777,11 +777,12 @@ bool out_map(CUtensorMap* m, void* out, int64_t rows, int64_t cols, bool gate) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Rows of capacity an expert from which on pairs of CTAs take a tile.  Both forms with 128 experts and blocks of 16, us,
-// single | pair: 4096 -> 2816 gated, 8 rows an expert 127 | 132, 48 rows 132 | 138, 64 rows 161 | 139, 128 rows
+// Rows of capacity an expert from which on pairs of CTAs take a tile.  Both forms with 128 experts and blocks of 16,
+// us, single | pair: 4096 -> 2816 gated, 8 rows an expert 127 | 132, 48 rows 132 | 138, 64 rows 161 | 139, 128 rows
 // 266 | 151; 768 -> 2048, 8 rows 22.6 | 23.9, 48 rows 25.4 | 26.3, 64 rows 31.9 | 27.4, 128 rows 50.8 | 32.1; one token of
-// six experts 4.7 | 5.7.  (A single CTA's tile ends at 64 rows.  The host knows the capacity, rows and padding; where
-// padding makes the most of it, 2 rows in blocks of 128, the pair costs 0 to 5 %.)
+// six experts 4.7 | 5.7.  (A single CTA's tile ends at 64 rows.  The host knows the capacity only: all T k slots, other
+// ranks' among them, and padding.  A rank with an eighth of the experts takes pairs from 8 rows an expert on, which by
+// the sweep costs it 3.5 to 6 % below 64; where padding makes the most of it, 2 rows in blocks of 128, 0 to 5 %.)
 constexpr int kPairRows = 64;
 
 template <int CG, bool kGate>

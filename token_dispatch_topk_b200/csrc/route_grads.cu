@@ -300,9 +300,9 @@ __device__ __forceinline__ Slots take_slots(const GateGradArgs& a, int64_t t0, i
 
 // Only the selected experts' logits have a gradient: a warp takes as many rows as its lanes have room for their slots,
 // sends zeros to the rows at once, while the slots (and, for the logistic, the scattered logits) are on their way, and
-// then writes the selected elements over them.  Bound by the T E elements written and, for the logistic, by a DRAM
-// sector per selected logit.  65536 x 256 bf16, k = 8: 13.6 us; 16.7 us with the rows put together in shared
-// memory first.
+// then writes the selected elements over them.  Bound by the T E elements written and, for the logistic, by the
+// 128-byte lines that hold the selected logits (eight of 256 bf16 logits lie in 3.6 of a row's four lines).  65536 x
+// 256 bf16, k = 8: 13.6 us; 16.7 us with the rows put together in shared memory first.
 template <typename TX, int VEC>
 __global__ void __launch_bounds__(kGateWarps * 32) gate_grad_sparse_kernel(GateGradArgs a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.E;
@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_grad_sparse_kernel(GateG
 // The softmax over all experts: every logit has a gradient.  A row takes G lanes, CPL vectors each; a warp takes
 // a.iters (at most R, and R CPL VEC <= 32 registers) times 32 / G rows, all read first of all; the selected experts' g_j
 // go into the rows' fp32 sums in shared memory meanwhile; the probabilities are recomputed.  Small batches wait for two
-// dependent loads (16384 x 60 fp32: 4.5 us, 5.9 with one group of rows a warp), large ones for the chain of shuffles and
+// dependent loads (16384 x 60 fp32: 4.7 us, 5.9 with one group of rows a warp), large ones for the chain of shuffles and
 // exponentials of a row (65536 x 256 bf16: 37 us, 48 with one group, against 11 at the copy rate).  At most 64 registers:
 // 37 us against 40.
 constexpr int kDenseRows = 64;  // of a warp, at most

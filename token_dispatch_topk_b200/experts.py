@@ -4,7 +4,8 @@
            --moe_quantize_mx4--> 4-bit rows --moe_grouped_gemm_mx4--> expert outputs, for moe_combine
 
 The weights are quantised once, at construction; every buffer is preallocated for the router's sizes, so that a step
-(``MoeRouter.step_mx4``) neither allocates nor synchronises and can be captured in a CUDA graph.
+(``MoeRouter.step_mx4``) neither allocates nor synchronises and can be captured in a CUDA graph.  Steps that may run at
+the same time (on two streams, or two captured graphs) need objects, and routers, of their own.
 """
 from __future__ import annotations
 

@@ -78,7 +78,8 @@ class MoeRouter:
                          topk_weights: Optional[torch.Tensor] = None, stream=None):
         """The combine's gradients for the step's routes: (grad_expert_out, grad_topk_weights), both this router's
         buffers.  The pad rows of grad_expert_out below N_pad are +0, so products over whole blocks may use it.
-        Under expert parallelism the weights' gradient of a remote slot is 0 here: sum it over the ranks."""
+        Routes given by the caller need their topk_weights here too.  Under expert parallelism the weights' gradient of a
+        remote slot is 0 here: sum it over the ranks."""
         self._needs_training()
         w = self.topk_weights if topk_weights is None else topk_weights
         return B.moe_combine_backward(grad_out, expert_out, w, self.align.inv_perm, self.grad_expert_out,
@@ -87,14 +88,17 @@ class MoeRouter:
                                       stream=stream)
 
     def gather_backward(self, grad_permuted: torch.Tensor, stream=None) -> torch.Tensor:
-        """The permute-gather's gradient: grad_hidden, this router's buffer."""
+        """The permute-gather's gradient: grad_hidden, this router's buffer.  Under expert parallelism it sums this rank's
+        experts' rows only (+0 for a token without one): sum it over the ranks."""
         self._needs_training()
         return B.moe_gather_backward(grad_permuted, self.align.inv_perm, self.k, self.grad_hidden,
                                      device_status=self.workspace, stream=stream)
 
     def gate_backward(self, logits: torch.Tensor, grad_topk_weights: Optional[torch.Tensor] = None,
                       stream=None) -> torch.Tensor:
-        """The gating's gradient, by default from combine_backward's weights: grad_logits, this router's buffer."""
+        """The gating's gradient, by default from combine_backward's weights: grad_logits, this router's buffer.  For the
+        routes that ``gate``, ``dispatch`` or a step chose from these logits, not for routes given by the caller.  Under
+        expert parallelism pass the weights' gradient summed over the ranks."""
         self._needs_training()
         g = self.grad_topk_weights if grad_topk_weights is None else grad_topk_weights
         return B.moe_topk_softmax_backward(g, logits, self.topk_weights, self.topk_ids, self.renormalize,
